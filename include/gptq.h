@@ -71,7 +71,13 @@ enum gptq_op {
   GPTQ_OP_ACCUMULATE = 0, /* sizes: rows ignored, cols = d, n = tokens         */
   GPTQ_OP_PREPARE = 1,    /* sizes: rows ignored, cols = d, n ignored          */
   GPTQ_OP_QUANTIZE = 2,   /* sizes: rows, cols, n ignored                       */
-  GPTQ_OP_QUANTIZE_PERM = 3 /* gptq_quantize_layer_perm: rows, cols, n ignored    */
+  GPTQ_OP_QUANTIZE_PERM = 3, /* gptq_quantize_layer_perm: rows, cols, n ignored    */
+  /* sized by gptq_adapters_workspace_bytes */
+  GPTQ_OP_FORWARD_ADAPTERS = 4, /* gptq_dequant_gemm_adapters, gptq_linear_forward_adapters */
+  GPTQ_OP_BACKWARD = 5,         /* gptq_linear_backward                             */
+  /* sized by gptq_head_workspace_bytes */
+  GPTQ_OP_HEAD_LOSS = 6,    /* gptq_head_loss, gptq_head_distill                    */
+  GPTQ_OP_HEAD_BACKWARD = 7 /* gptq_head_loss_backward, gptq_head_distill_backward  */
 };
 
 /* Library version (major*10000 + minor*100 + patch). */
@@ -413,6 +419,182 @@ gptq_status gptq_linear_forward(const void* x, int64_t m, int64_t cols, int64_t 
  */
 gptq_status gptq_hessian_accumulate_noalloc(float* H, int64_t d, const void* X, int64_t n,
                                             int64_t ldx, float alpha, void* stream);
+
+/*
+ * Low-rank adapters beside a stored layer.  Many requests share one stored
+ * layer, each with a small correction of its own; a token t with
+ * a = index[t] in [0, count) gets
+ *
+ *     y_t = W_hat x_t + scaling[a] * B[a] (A[a] x_t),
+ *
+ * one with any other index (say -1) the layer's own product.  The stored
+ * weights stay as they are; A and B are what is trained
+ * (gptq_linear_backward).  An adapter of a smaller rank is stored with zero
+ * rows in A.
+ *
+ *   A        count x rank x cols fp16
+ *   B        count x rows x rank fp16
+ *   scaling  count fp32
+ *   index    one int32 per token; in any order, but the products for many
+ *            tokens and the gradients are fastest when a request's tokens
+ *            stand together (a tile of 128 tokens takes its adapters one
+ *            after another).
+ *   count    >= 1, at most 2^20 (gradients: 4096, else GPTQ_ERR_UNSUPPORTED)
+ *   rank     >= 1, at most 128 (else GPTQ_ERR_UNSUPPORTED)
+ * A[a] x_t and everything after it is fp32; an infinity or NaN in one adapter
+ * reaches only its own tokens.
+ */
+typedef struct gptq_adapters {
+  const void* A;
+  const void* B;
+  const float* scaling;
+  const int32_t* index;
+  int64_t count;
+  int rank;
+} gptq_adapters;
+
+/* Bytes of workspace for m tokens (op: GPTQ_OP_FORWARD_ADAPTERS or
+ * GPTQ_OP_BACKWARD; count = rank = 0 without adapters); 0 for sizes the
+ * operation would reject. */
+size_t gptq_adapters_workspace_bytes(int op, int64_t m, int64_t rows, int64_t cols, int64_t count,
+                                     int rank);
+
+/*
+ * gptq_dequant_gemm_adapters -- gptq_dequant_gemm (a few tokens, fp32 y, any
+ * bits, group size and g_idx it takes) with the tokens' adapters.  The
+ * layer's part has gptq_dequant_gemm's bound; the adapter's part is within
+ * (cols + rank + 8) * 2^-24 * |scaling| * sum_j |B_j| sum_c |A_jc x_c|.
+ *   m          at most 2^23 (else GPTQ_ERR_UNSUPPORTED); 0 is a no-op.
+ *   Asynchronous; bitwise deterministic.
+ */
+gptq_status gptq_dequant_gemm_adapters(const void* x, int64_t m, int64_t cols, int64_t ldx,
+                                       const uint32_t* packed, int bits, int64_t rows,
+                                       const float* scales, const float* zeros, int groupsize,
+                                       const int32_t* g_idx, const gptq_adapters* adapters,
+                                       float* y, int64_t ldy, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/*
+ * gptq_linear_forward_adapters -- gptq_linear_forward (many tokens, fp16 y;
+ * the same shapes, alignment and errors) with the tokens' adapters:
+ * y = act(x W_hat^T + adapters).  The fp32 sum is rounded to fp16 (a token
+ * without an adapter can differ by one fp16 step from gptq_linear_forward
+ * without ReLU, whose last addition rounds straight to fp16).
+ *   Asynchronous; bitwise deterministic.
+ */
+gptq_status gptq_linear_forward_adapters(const void* x, int64_t m, int64_t cols, int64_t ldx,
+                                         const uint32_t* packed, int bits, int64_t rows,
+                                         const float* scales, const float* zeros, int groupsize,
+                                         int relu, const gptq_adapters* adapters, void* y,
+                                         int64_t ldy, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
+/*
+ * gptq_linear_backward -- the gradient through a stored layer, and its
+ * adapters' gradients.  With dv_t = scaling[a] B[a]^T dy_t, a = index[t]:
+ *
+ *     dx_t = W_hat^T dy_t + A[a]^T dv_t
+ *     dA[a] = sum_{t: index[t] = a} dv_t x_t^T
+ *     dB[a] = sum_{t: index[t] = a} scaling[a] dy_t (A[a] x_t)^T
+ *
+ * The stored weights have no gradient.  Where the forward product had
+ * relu = 1, dy is the gradient before it (zero where y is 0).
+ *
+ *   dy         m x rows fp16, row t at dy + t*lddy (lddy >= rows; where
+ *              rows % 64 == 0 also lddy % 8 == 0 and dy 16-byte aligned, else
+ *              GPTQ_ERR_UNSUPPORTED); m at most 2^23.
+ *   packed, bits, scales, zeros, groupsize, g_idx   as gptq_dequant_gemm
+ *              (bits 2..8, any group size).
+ *   adapters   NULL: dx = W_hat^T dy alone; x, dA and dB are not read.
+ *   x          m x cols fp16, the forward product's input.
+ *   dx         m x cols fp16 out, row t at dx + t*lddx.
+ *   dA, dB     fp32 out in A's and B's layouts, overwritten; 0 for an adapter
+ *              without tokens (all of them when m = 0).
+ *   Arithmetic: for dx W_hat is rounded to fp16 (2^-11 relative, 2^-25 below
+ *   2^-14; values beyond 65504 become infinite), products are exact in fp32
+ *   and summed there, and dx is rounded to fp16 once.  The adapters' parts
+ *   are fp32 throughout; their sums run over an adapter's tokens in token
+ *   order, 256 at a time, so results are bitwise reproducible.
+ *   Asynchronous.
+ */
+gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_t lddy,
+                                 const uint32_t* packed, int bits, int64_t cols,
+                                 const float* scales, const float* zeros, int groupsize,
+                                 const int32_t* g_idx, const gptq_adapters* adapters,
+                                 const void* x, int64_t ldx, void* dx, int64_t lddx, float* dA,
+                                 float* dB, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * Losses through a stored vocabulary projection (rows = vocabulary entries),
+ * z = W_hat h.  The logits are never kept: a piece of at most 8192 entries
+ * (2^25 probabilities) is in the workspace at a time.
+ *
+ * gptq_head_loss -- softmax cross entropy, loss[t] = lse(z_t) - z_t[y_t]: the
+ * training loss, and the score behind a perplexity.
+ * gptq_head_distill -- distillation from a teacher's largest logits: with
+ * p = softmax(top_logits / T) over the token's entries and z = W_hat h / T,
+ * loss[t] = sum_k p_k (log p_k - z_k + lse(z_t)).
+ * The _backward calls give dh[t] = dloss[t] * d loss[t] / d h[t], from what
+ * the forward call left in lse and target_logit (student_logits).
+ *
+ *   h            m x cols fp16, and the layer: shapes, alignment and errors
+ *                of gptq_linear_forward (4 or 8 bits); m at most 2^23.
+ *   target       m int32; outside [0, rows), say -100: the token takes no
+ *                part (loss and gradient 0, whatever h holds).
+ *   top_index,   m x top int32 and fp32 (row stride top), top in 1..256
+ *   top_logits   (above: GPTQ_ERR_UNSUPPORTED), in any order.  An entry takes
+ *                part if its index lies in [0, rows) and its logit is not
+ *                -inf; a token without entries takes no part.  An index given
+ *                twice counts as two entries.
+ *   temperature  T > 0 (finite, and 1 / T).  The loss is not scaled by T^2:
+ *                pass that in dloss.
+ *   loss, lse    m fp32 out: the loss and lse(z_t) (natural logarithm).
+ *   target_logit m fp32 out (student_logits: m x top): z of the entries, 0
+ *                for those that take no part.
+ *   dloss        m fp32: the weight of each token's loss (1 / tokens, times
+ *                a loss scale that keeps dh inside fp16).
+ *   dh           m x cols fp16 out, row t at dh + t*lddh.
+ *   Arithmetic: z is formed as gptq_linear_forward forms its sums, without a
+ *   rounding to fp16; exp, log and their sums are fp32.  For dh, the
+ *   probabilities (p - target in fp32 first) and W_hat are rounded to fp16
+ *   (2^-11 relative, 2^-25 below 2^-14), products and sums are fp32, and dh
+ *   is rounded to fp16 once.
+ *   Asynchronous; bitwise deterministic.
+ */
+gptq_status gptq_head_loss(const void* h, int64_t m, int64_t cols, int64_t ldh,
+                           const uint32_t* packed, int bits, int64_t rows, const float* scales,
+                           const float* zeros, int groupsize, const int32_t* target, float* loss,
+                           float* lse, float* target_logit, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+gptq_status gptq_head_loss_backward(const void* h, int64_t m, int64_t cols, int64_t ldh,
+                                    const uint32_t* packed, int bits, int64_t rows,
+                                    const float* scales, const float* zeros, int groupsize,
+                                    const int32_t* target, const float* lse,
+                                    const float* target_logit, const float* dloss, void* dh,
+                                    int64_t lddh, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+gptq_status gptq_head_distill(const void* h, int64_t m, int64_t cols, int64_t ldh,
+                              const uint32_t* packed, int bits, int64_t rows, const float* scales,
+                              const float* zeros, int groupsize, const int32_t* top_index,
+                              const float* top_logits, int top, float temperature, float* loss,
+                              float* lse, float* student_logits, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+gptq_status gptq_head_distill_backward(const void* h, int64_t m, int64_t cols, int64_t ldh,
+                                       const uint32_t* packed, int bits, int64_t rows,
+                                       const float* scales, const float* zeros, int groupsize,
+                                       const int32_t* top_index, const float* top_logits, int top,
+                                       float temperature, const float* lse,
+                                       const float* student_logits, const float* dloss, void* dh,
+                                       int64_t lddh, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/* Bytes of workspace of the calls above (op: GPTQ_OP_HEAD_LOSS or
+ * GPTQ_OP_HEAD_BACKWARD); 0 for sizes the operation would reject. */
+size_t gptq_head_workspace_bytes(int op, int64_t m, int64_t rows, int64_t cols);
 
 #ifdef __cplusplus
 }

@@ -37,3 +37,12 @@ from .pipeline64 import (  # noqa: F401
     quantized_layer_output,
     two_layer_block,
 )
+from .train64 import (  # noqa: F401
+    adapter_of,
+    adapters_forward,
+    adapters_backward,
+    head_targets,
+    head_loss,
+    head_dz,
+    head_backward,
+)

@@ -16,15 +16,29 @@ from ._lib import (  # noqa: F401
     GPTQ_OK,
     LIB_PATH,
     OP_ACCUMULATE,
+    OP_BACKWARD,
+    OP_FORWARD_ADAPTERS,
+    OP_HEAD_BACKWARD,
+    OP_HEAD_LOSS,
     OP_PREPARE,
     OP_QUANTIZE,
     OP_QUANTIZE_PERM,
     act_order,
+    adapters_workspace_bytes,
     dequant_gemm,
+    dequant_gemm_adapters,
+    head_distill,
+    head_distill_backward,
+    head_loss,
+    head_loss_backward,
+    head_workspace_bytes,
     hessian_accumulate,
     hessian_accumulate_noalloc,
     lib,
+    linear_backward,
+    linear_backward_adapters,
     linear_forward,
+    linear_forward_adapters,
     pack_codes,
     packed_words,
     prepare_hinv,

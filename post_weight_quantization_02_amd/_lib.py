@@ -27,6 +27,10 @@ OP_ACCUMULATE = 0
 OP_PREPARE = 1
 OP_QUANTIZE = 2
 OP_QUANTIZE_PERM = 3
+OP_FORWARD_ADAPTERS = 4
+OP_BACKWARD = 5
+OP_HEAD_LOSS = 6
+OP_HEAD_BACKWARD = 7
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(
@@ -81,6 +85,38 @@ lib.gptq_hessian_accumulate_noalloc.argtypes = [_p, _i64, _p, _i64, _i64, ctypes
 lib.gptq_quantize_layer_perm.restype = _int
 lib.gptq_quantize_layer_perm.argtypes = [_p, _int, _i64, _i64, _i64, _p, _p, _int, _int, _int,
                                          _p, _p, _p, _p, _p, _p, _sz, _p]
+
+
+class _Adapters(ctypes.Structure):  # gptq_adapters
+    _fields_ = [("A", _p), ("B", _p), ("scaling", _p), ("index", _p), ("count", _i64),
+                ("rank", _int)]
+
+
+_f = ctypes.c_float
+_ad = ctypes.POINTER(_Adapters)
+lib.gptq_adapters_workspace_bytes.restype = _sz
+lib.gptq_adapters_workspace_bytes.argtypes = [_int, _i64, _i64, _i64, _i64, _int]
+lib.gptq_head_workspace_bytes.restype = _sz
+lib.gptq_head_workspace_bytes.argtypes = [_int, _i64, _i64, _i64]
+lib.gptq_dequant_gemm_adapters.restype = _int
+lib.gptq_dequant_gemm_adapters.argtypes = [_p, _i64, _i64, _i64, _p, _int, _i64, _p, _p, _int, _p,
+                                           _ad, _p, _i64, _p, _sz, _p]
+lib.gptq_linear_forward_adapters.restype = _int
+lib.gptq_linear_forward_adapters.argtypes = [_p, _i64, _i64, _i64, _p, _int, _i64, _p, _p, _int,
+                                             _int, _ad, _p, _i64, _p, _sz, _p]
+lib.gptq_linear_backward.restype = _int
+lib.gptq_linear_backward.argtypes = [_p, _i64, _i64, _i64, _p, _int, _i64, _p, _p, _int, _p, _ad,
+                                     _p, _i64, _p, _i64, _p, _p, _p, _sz, _p]
+_head = [_p, _i64, _i64, _i64, _p, _int, _i64, _p, _p, _int]  # h and the layer
+lib.gptq_head_loss.restype = _int
+lib.gptq_head_loss.argtypes = _head + [_p, _p, _p, _p, _p, _sz, _p]
+lib.gptq_head_loss_backward.restype = _int
+lib.gptq_head_loss_backward.argtypes = _head + [_p, _p, _p, _p, _p, _i64, _p, _sz, _p]
+lib.gptq_head_distill.restype = _int
+lib.gptq_head_distill.argtypes = _head + [_p, _p, _int, _f, _p, _p, _p, _p, _sz, _p]
+lib.gptq_head_distill_backward.restype = _int
+lib.gptq_head_distill_backward.argtypes = _head + [_p, _p, _int, _f, _p, _p, _p, _p, _i64, _p, _sz,
+                                                   _p]
 
 
 class GPTQError(RuntimeError):
@@ -459,3 +495,290 @@ def linear_forward(x, packed, bits: int, cols: int, scales, zeros, groupsize: in
                                  _stream_ptr(stream, x.device))
     _check(st, "gptq_linear_forward")
     return out
+
+
+# ------------------------------------------- adapters, gradients, vocabulary losses
+def adapters_workspace_bytes(op: int, m: int, rows: int, cols: int, count: int = 0,
+                             rank: int = 0) -> int:
+    """Workspace of OP_FORWARD_ADAPTERS or OP_BACKWARD for m tokens."""
+    return int(lib.gptq_adapters_workspace_bytes(op, m, rows, cols, count, rank))
+
+
+def head_workspace_bytes(op: int, m: int, rows: int, cols: int) -> int:
+    """Workspace of OP_HEAD_LOSS or OP_HEAD_BACKWARD for m tokens."""
+    return int(lib.gptq_head_workspace_bytes(op, m, rows, cols))
+
+
+def _rows_of(t, m, n, dtype, device, name):
+    """An m x n matrix with unit column stride; returns its row stride."""
+    if t.dtype != dtype or t.device != device or t.dim() != 2 or tuple(t.shape) != (m, n) or \
+            (n > 1 and m > 0 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be an {m} x {n} {dtype} tensor with unit column stride "
+                         f"on {device}")
+    return t.stride(0) if m > 1 else n
+
+
+def _layer(packed, bits, cols, scales, zeros, groupsize, device, g_idx=None):
+    """The stored layer's checks; returns (rows, groupsize, g_idx)."""
+    torch = _torch()
+    if packed.dim() != 2 or packed.dtype != torch.int32 or not packed.is_contiguous() or \
+            packed.device != device or packed.shape[1] != packed_words(cols, bits):
+        raise ValueError("packed must come from pack_codes for these cols and bits")
+    rows = packed.shape[0]
+    if groupsize <= 0:
+        groupsize = cols
+    ng = (cols + groupsize - 1) // groupsize
+    for t in (scales, zeros):
+        if t.dtype != torch.float32 or tuple(t.shape) != (rows, ng) or not t.is_contiguous() or \
+                t.device != device:
+            raise ValueError("scales and zeros must be contiguous rows x ngroups fp32")
+    return rows, groupsize, _check_perm(g_idx, cols, device)
+
+
+def _adapters(A, B, scaling, index, m, rows, cols, device):
+    """The adapters' checks; returns the C struct."""
+    torch = _torch()
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A must be count x rank x cols and B count x rows x rank")
+    count, rank = A.shape[0], A.shape[1]
+    for t, shape, dtype, name in ((A, (count, rank, cols), torch.float16, "A"),
+                                  (B, (count, rows, rank), torch.float16, "B"),
+                                  (scaling, (count,), torch.float32, "scaling"),
+                                  (index, (m,), torch.int32, "index")):
+        if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or \
+                not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} "
+                             f"on {device}")
+    return _Adapters(A.data_ptr(), B.data_ptr(), scaling.data_ptr(), index.data_ptr(), count, rank)
+
+
+def _out_rows(out, m, n, dtype, device):
+    """(out, its row stride), allocated when None."""
+    torch = _torch()
+    if out is None:
+        out = torch.empty((m, n), dtype=dtype, device=device)
+    return out, _rows_of(out, m, n, dtype, device, "out")
+
+
+def _x_rows(x, cols, name="x"):
+    torch = _torch()
+    if x.dtype != torch.float16 or not x.is_cuda or x.dim() != 2 or x.shape[1] != cols:
+        raise ValueError(f"{name} must be an m x cols fp16 CUDA tensor with unit column stride")
+    return x.shape[0], _rows_of(x, x.shape[0], cols, torch.float16, x.device, name)
+
+
+def dequant_gemm_adapters(x, packed, bits: int, cols: int, scales, zeros, groupsize: int, A, B,
+                          scaling, index, g_idx=None, out=None, workspace=None, stream=None):
+    """dequant_gemm (m x rows fp32) with each token's low-rank adapter:
+    y_t += scaling[a] B[a] (A[a] x_t), a = index[t]; an index outside
+    [0, count) adds nothing. A: count x rank x cols and B: count x rows x rank
+    fp16, scaling: count fp32, index: m int32 (gptq_dequant_gemm_adapters)."""
+    torch = _torch()
+    m, ldx = _x_rows(x, cols)
+    rows, groupsize, g_idx = _layer(packed, bits, cols, scales, zeros, groupsize, x.device, g_idx)
+    ad = _adapters(A, B, scaling, index, m, rows, cols, x.device)
+    out, ldy = _out_rows(out, m, rows, torch.float32, x.device)
+    ws, wsb = _workspace(adapters_workspace_bytes(OP_FORWARD_ADAPTERS, m, rows, cols, ad.count,
+                                                  ad.rank), x.device, workspace, stream)
+    with torch.cuda.device(x.device):
+        st = lib.gptq_dequant_gemm_adapters(
+            x.data_ptr(), m, cols, ldx, packed.data_ptr(), bits, rows, scales.data_ptr(),
+            zeros.data_ptr(), groupsize, g_idx.data_ptr() if g_idx is not None else None,
+            ctypes.byref(ad), out.data_ptr(), ldy, ws.data_ptr() if ws is not None else None, wsb,
+            _stream_ptr(stream, x.device))
+    _check(st, "gptq_dequant_gemm_adapters")
+    return out
+
+
+def linear_forward_adapters(x, packed, bits: int, cols: int, scales, zeros, groupsize: int, A, B,
+                            scaling, index, relu: bool = False, out=None, workspace=None,
+                            stream=None):
+    """linear_forward (m x rows fp16, many tokens) with each token's low-rank
+    adapter, as dequant_gemm_adapters (gptq_linear_forward_adapters)."""
+    torch = _torch()
+    m, ldx = _x_rows(x, cols)
+    rows, groupsize, _ = _layer(packed, bits, cols, scales, zeros, groupsize, x.device)
+    ad = _adapters(A, B, scaling, index, m, rows, cols, x.device)
+    out, ldy = _out_rows(out, m, rows, torch.float16, x.device)
+    ws, wsb = _workspace(adapters_workspace_bytes(OP_FORWARD_ADAPTERS, m, rows, cols, ad.count,
+                                                  ad.rank), x.device, workspace, stream)
+    with torch.cuda.device(x.device):
+        st = lib.gptq_linear_forward_adapters(
+            x.data_ptr(), m, cols, ldx, packed.data_ptr(), bits, rows, scales.data_ptr(),
+            zeros.data_ptr(), groupsize, 1 if relu else 0, ctypes.byref(ad), out.data_ptr(), ldy,
+            ws.data_ptr() if ws is not None else None, wsb, _stream_ptr(stream, x.device))
+    _check(st, "gptq_linear_forward_adapters")
+    return out
+
+
+def _backward(dy, x, layer, adapters, g_idx, out, dA, dB, workspace, stream):
+    torch = _torch()
+    packed, bits, cols, scales, zeros, groupsize = layer
+    if dy.dtype != torch.float16 or not dy.is_cuda or dy.dim() != 2:
+        raise ValueError("dy must be an m x rows fp16 CUDA tensor with unit column stride")
+    m, dev = dy.shape[0], dy.device
+    rows, groupsize, g_idx = _layer(packed, bits, cols, scales, zeros, groupsize, dev, g_idx)
+    lddy = _rows_of(dy, m, rows, torch.float16, dev, "dy")
+    out, lddx = _out_rows(out, m, cols, torch.float16, dev)
+    ad, ldx, count, rank = None, 0, 0, 0
+    if adapters is not None:
+        ldx = _rows_of(x, m, cols, torch.float16, dev, "x")
+        ad = _adapters(*adapters, m, rows, cols, dev)
+        count, rank = ad.count, ad.rank
+        if dA is None:
+            dA = torch.empty((count, rank, cols), dtype=torch.float32, device=dev)
+        if dB is None:
+            dB = torch.empty((count, rows, rank), dtype=torch.float32, device=dev)
+        _check_out(dA, (count, rank, cols), torch.float32, dev, "dA")
+        _check_out(dB, (count, rows, rank), torch.float32, dev, "dB")
+    ws, wsb = _workspace(adapters_workspace_bytes(OP_BACKWARD, m, rows, cols, count, rank), dev,
+                         workspace, stream)
+    with torch.cuda.device(dev):
+        st = lib.gptq_linear_backward(
+            dy.data_ptr(), m, rows, lddy, packed.data_ptr(), bits, cols, scales.data_ptr(),
+            zeros.data_ptr(), groupsize, g_idx.data_ptr() if g_idx is not None else None,
+            ctypes.byref(ad) if ad is not None else None, x.data_ptr() if ad is not None else None,
+            ldx, out.data_ptr(), lddx, dA.data_ptr() if ad is not None else None,
+            dB.data_ptr() if ad is not None else None, ws.data_ptr() if ws is not None else None,
+            wsb, _stream_ptr(stream, dev))
+    _check(st, "gptq_linear_backward")
+    return out, dA, dB
+
+
+def linear_backward(dy, packed, bits: int, cols: int, scales, zeros, groupsize: int, g_idx=None,
+                    out=None, workspace=None, stream=None):
+    """dx = dy W_hat (m x cols fp16) for dy m x rows fp16: the gradient
+    through a stored layer (gptq_linear_backward without adapters)."""
+    return _backward(dy, None, (packed, bits, cols, scales, zeros, groupsize), None, g_idx, out,
+                     None, None, workspace, stream)[0]
+
+
+def linear_backward_adapters(dy, x, packed, bits: int, cols: int, scales, zeros, groupsize: int, A,
+                             B, scaling, index, g_idx=None, out=None, dA=None, dB=None,
+                             workspace=None, stream=None):
+    """(dx m x cols fp16, dA count x rank x cols fp32, dB count x rows x rank
+    fp32) of the product with adapters for its input x and dy (m x rows fp16);
+    where the forward product had relu, dy is zero where its output is 0
+    (gptq_linear_backward)."""
+    return _backward(dy, x, (packed, bits, cols, scales, zeros, groupsize),
+                     (A, B, scaling, index), g_idx, out, dA, dB, workspace, stream)
+
+
+def _head_targets(index, logits, m, device):
+    """(top, checked tensors) of labels (logits None) or of a teacher's entries."""
+    torch = _torch()
+    if logits is None:
+        if index.dtype != torch.int32 or tuple(index.shape) != (m,) or index.device != device or \
+                not index.is_contiguous():
+            raise ValueError(f"target must be a contiguous int32 tensor of length {m} on {device}")
+        return 1
+    if index.dim() != 2:
+        raise ValueError("top_index must be m x top")
+    shape = (m, index.shape[1])
+    for t, dtype, name in ((index, torch.int32, "top_index"), (logits, torch.float32, "top_logits")):
+        if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or \
+                not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous m x top {dtype} tensor on {device}")
+    return shape[1]
+
+
+def _head_forward(h, layer, index, logits, temperature, loss, lse, zk, workspace, stream):
+    torch = _torch()
+    packed, bits, cols, scales, zeros, groupsize = layer
+    m, ldh = _x_rows(h, cols, "h")
+    dev = h.device
+    rows, groupsize, _ = _layer(packed, bits, cols, scales, zeros, groupsize, dev)
+    top = _head_targets(index, logits, m, dev)
+    shape = (m,) if logits is None else (m, top)
+    if loss is None:
+        loss = torch.empty((m,), dtype=torch.float32, device=dev)
+    if lse is None:
+        lse = torch.empty((m,), dtype=torch.float32, device=dev)
+    if zk is None:
+        zk = torch.empty(shape, dtype=torch.float32, device=dev)
+    _check_out(loss, (m,), torch.float32, dev, "loss")
+    _check_out(lse, (m,), torch.float32, dev, "lse")
+    _check_out(zk, shape, torch.float32, dev, "the entries' logits")
+    ws, wsb = _workspace(head_workspace_bytes(OP_HEAD_LOSS, m, rows, cols), dev, workspace, stream)
+    head = (h.data_ptr(), m, cols, ldh, packed.data_ptr(), bits, rows, scales.data_ptr(),
+            zeros.data_ptr(), groupsize, index.data_ptr())
+    tail = (loss.data_ptr(), lse.data_ptr(), zk.data_ptr(),
+            ws.data_ptr() if ws is not None else None, wsb, _stream_ptr(stream, dev))
+    with torch.cuda.device(dev):
+        if logits is None:
+            st, name = lib.gptq_head_loss(*head, *tail), "gptq_head_loss"
+        else:
+            st = lib.gptq_head_distill(*head, logits.data_ptr(), top, temperature, *tail)
+            name = "gptq_head_distill"
+    _check(st, name)
+    return loss, lse, zk
+
+
+def _head_backward(h, layer, index, logits, temperature, lse, zk, dloss, out, workspace, stream):
+    torch = _torch()
+    packed, bits, cols, scales, zeros, groupsize = layer
+    m, ldh = _x_rows(h, cols, "h")
+    dev = h.device
+    rows, groupsize, _ = _layer(packed, bits, cols, scales, zeros, groupsize, dev)
+    top = _head_targets(index, logits, m, dev)
+    _check_out(lse, (m,), torch.float32, dev, "lse")
+    _check_out(zk, (m,) if logits is None else (m, top), torch.float32, dev, "the entries' logits")
+    _check_out(dloss, (m,), torch.float32, dev, "dloss")
+    out, lddh = _out_rows(out, m, cols, torch.float16, dev)
+    ws, wsb = _workspace(head_workspace_bytes(OP_HEAD_BACKWARD, m, rows, cols), dev, workspace,
+                         stream)
+    head = (h.data_ptr(), m, cols, ldh, packed.data_ptr(), bits, rows, scales.data_ptr(),
+            zeros.data_ptr(), groupsize, index.data_ptr())
+    tail = (lse.data_ptr(), zk.data_ptr(), dloss.data_ptr(), out.data_ptr(), lddh,
+            ws.data_ptr() if ws is not None else None, wsb, _stream_ptr(stream, dev))
+    with torch.cuda.device(dev):
+        if logits is None:
+            st, name = lib.gptq_head_loss_backward(*head, *tail), "gptq_head_loss_backward"
+        else:
+            st = lib.gptq_head_distill_backward(*head, logits.data_ptr(), top, temperature, *tail)
+            name = "gptq_head_distill_backward"
+    _check(st, name)
+    return out
+
+
+def head_loss(h, packed, bits: int, cols: int, scales, zeros, groupsize: int, target, loss=None,
+              lse=None, target_logit=None, workspace=None, stream=None):
+    """Softmax cross entropy through a stored vocabulary projection, logits
+    not kept: (loss, lse, target_logit), m fp32 each, for hidden states h
+    (m x cols fp16) and labels target (m int32; outside [0, rows): the token
+    takes no part). lse and target_logit are what head_loss_backward takes
+    (gptq_head_loss)."""
+    return _head_forward(h, (packed, bits, cols, scales, zeros, groupsize), target, None, 1.0, loss,
+                         lse, target_logit, workspace, stream)
+
+
+def head_loss_backward(h, packed, bits: int, cols: int, scales, zeros, groupsize: int, target, lse,
+                       target_logit, dloss, out=None, workspace=None, stream=None):
+    """dh (m x cols fp16) of sum_t dloss[t] * loss[t] (gptq_head_loss_backward)."""
+    return _head_backward(h, (packed, bits, cols, scales, zeros, groupsize), target, None, 1.0, lse,
+                          target_logit, dloss, out, workspace, stream)
+
+
+def head_distill(h, packed, bits: int, cols: int, scales, zeros, groupsize: int, top_index,
+                 top_logits, temperature: float = 1.0, loss=None, lse=None, student_logits=None,
+                 workspace=None, stream=None):
+    """Distillation from a teacher's largest logits through a stored
+    vocabulary projection: (loss m, lse m, student_logits m x top, fp32) for
+    top_index (int32) and top_logits (fp32), m x top; an index outside
+    [0, rows) or a logit of -inf marks an entry that is not there
+    (gptq_head_distill)."""
+    if not (temperature > 0 and 1e-30 < temperature < 1e30):
+        raise ValueError("temperature must be positive")
+    return _head_forward(h, (packed, bits, cols, scales, zeros, groupsize), top_index, top_logits,
+                         float(temperature), loss, lse, student_logits, workspace, stream)
+
+
+def head_distill_backward(h, packed, bits: int, cols: int, scales, zeros, groupsize: int,
+                          top_index, top_logits, temperature, lse, student_logits, dloss, out=None,
+                          workspace=None, stream=None):
+    """dh (m x cols fp16) of sum_t dloss[t] * loss[t] of head_distill
+    (gptq_head_distill_backward)."""
+    if not (temperature > 0 and 1e-30 < temperature < 1e30):
+        raise ValueError("temperature must be positive")
+    return _head_backward(h, (packed, bits, cols, scales, zeros, groupsize), top_index, top_logits,
+                          float(temperature), lse, student_logits, dloss, out, workspace, stream)

@@ -13,7 +13,8 @@ LIB = os.path.join(HERE, "libgptq_mi355x.so")
 BUILD = os.path.join(HERE, "_build")
 
 SOURCES = ["gptq_abi.cpp", "syrk_f16.hip", "chol_f64.hip", "sweep.hip", "act_order.hip", "infer.hip",
-           "linear_mfma.hip", "accumulate_noalloc.hip"]
+           "linear_mfma.hip", "accumulate_noalloc.hip", "adapters.hip", "gemm_f16.hip", "head.hip",
+           "train_abi.cpp"]
 
 # Per-file code generation options.  The fp64 kernels keep their MFMA
 # accumulators in ordinary VGPRs: with the default AGPR form the compiler

@@ -1,0 +1,363 @@
+// Low-rank adapters of many requests beside one stored layer:
+//   y_t  = W_hat x_t + s_a B_a (A_a x_t),       a = index[t]
+// and the adapters' gradients, with dv_t = s_a B_a^T dy_t:
+//   dA_a = sum_{t: index[t] = a} dv_t x_t^T,    dB_a = sum dy_t v_t^T,
+// v_t = s_a A_a x_t.  A_a is rank x cols, B_a rows x rank (fp16); v and dv are
+// fp32, and every product below is exact in fp32 and summed in fp32.
+#include "adapters_dev.h"
+
+namespace gptq {
+namespace {
+
+// 8 values of a row of K values from k on, zero past its end.
+template <bool VEC>
+__device__ inline half8 load8(const _Float16* row, int64_t k, int64_t K) {
+  half8 v = {};
+  if (VEC) {  // K % 8 == 0, 16-byte aligned rows
+    if (k < K) v = *reinterpret_cast<const half8*>(row + k);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k + e < K) v[e] = row[k + e];
+  }
+  return v;
+}
+
+__device__ inline int valid_id(const int* index, int64_t t, int count) {
+  const int d = index[t];
+  return (d >= 0 && d < count) ? d : -1;
+}
+
+// v[t][j] for one token and four j per workgroup: a few tokens, each with an
+// adapter of its own (decode).  Bound by the read of the adapters' rows.
+template <bool VEC>
+__global__ __launch_bounds__(256) void shrink_rows_kernel(ShrinkJob job, int64_t m) {
+  __shared__ float red[4][4];
+  const int64_t t = blockIdx.x;
+  const int j0 = 4 * blockIdx.y;
+  const int a = valid_id(job.index, t, job.count);
+  float* out = job.v + t * job.ldv + j0;
+  if (a < 0) {  // the whole workgroup
+    if (threadIdx.x < 4) out[threadIdx.x] = 0.f;
+    return;
+  }
+  const _Float16* x = job.x + t * job.ldx;
+  const _Float16* down = job.down + a * job.stride;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int64_t k = (int64_t)threadIdx.x * 8; k < job.K; k += 256 * 8) {
+    const half8 xv = load8<VEC>(x, k, job.K);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (j0 + u >= job.rank) continue;
+      const half8 av = load8<VEC>(down + (j0 + u) * job.ldd, k, job.K);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[u] = __builtin_fmaf((float)xv[e], (float)av[e], acc[u]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) acc[u] += __shfl_xor(acc[u], o, 64);
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) red[wave][u] = acc[u];
+  __syncthreads();
+  if (threadIdx.x < 4) {
+    const int u = threadIdx.x;
+    const float sum = (red[0][u] + red[1][u]) + (red[2][u] + red[3][u]);
+    out[u] = j0 + u < job.rank ? job.scaling[a] * sum : 0.f;
+  }
+}
+
+// v for 16 tokens per workgroup on v_mfma_f32_16x16x32_f16 (tokens x rank
+// tiles of 16), the four waves taking every fourth run of 32 of K and their
+// sums added in wave order.  One pass per adapter found among the 16 tokens.
+template <bool VEC, int NB>
+__global__ __launch_bounds__(256) void shrink_tile_kernel(ShrinkJob j0, ShrinkJob j1, int64_t m) {
+  __shared__ float red[4][16][16 * NB + 1];
+  const ShrinkJob& job = blockIdx.y == 0 ? j0 : j1;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, kg = lane >> 4;
+  const int64_t t0 = (int64_t)blockIdx.x * 16;
+  const int id = t0 + li < m ? valid_id(job.index, t0 + li, job.count) : -1;
+  const _Float16* x = job.x + min(t0 + li, m - 1) * job.ldx;
+  // zeros where a token has no adapter, and behind the rank
+  for (int o = tid; o < 16 * job.ldv; o += 256) {
+    const int tok = o / job.ldv, j = o % job.ldv;
+    if (t0 + tok < m && (j >= job.rank || valid_id(job.index, t0 + tok, job.count) < 0))
+      job.v[(t0 + tok) * job.ldv + j] = 0.f;
+  }
+  int cur = -1;
+  while (true) {
+    int next = id > cur ? id : 0x7fffffff;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) next = min(next, __shfl_xor(next, o, 64));
+    cur = __builtin_amdgcn_readfirstlane(next);
+    if (cur == 0x7fffffff) break;  // the same in all four waves
+    const _Float16* down = job.down + cur * job.stride;
+    f32x4 acc[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int64_t k = 32 * wave + 8 * kg; k - 8 * kg < job.K; k += 128) {
+      const half8 xv = load8<VEC>(x, k, job.K);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        half8 dv = {};
+        if (16 * b + li < job.rank) dv = load8<VEC>(down + (16 * b + li) * job.ldd, k, job.K);
+        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv, dv, acc[b], 0, 0, 0);
+      }
+    }
+    __syncthreads();  // the previous turn's reads of red
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red[wave][4 * kg + i][16 * b + li] = acc[b][i];
+    __syncthreads();
+    const float s = job.scaling[cur];
+    for (int o = tid; o < 16 * 16 * NB; o += 256) {
+      const int tok = o / (16 * NB), j = o % (16 * NB);
+      if (t0 + tok < m && job.index[t0 + tok] == cur && j < job.rank)
+        job.v[(t0 + tok) * job.ldv + j] =
+            s * ((red[0][tok][j] + red[1][tok][j]) + (red[2][tok][j] + red[3][tok][j]));
+    }
+  }
+}
+
+// B_a (rows x rank) -> rank x ldt, the rows' order along the fast axis, zeros
+// from rows to ldt: the layout the shrink kernels read.
+__global__ __launch_bounds__(256) void transpose_up_kernel(const _Float16* __restrict__ B,
+                                                           int64_t rows, int rank, int64_t ldt,
+                                                           _Float16* __restrict__ Bt) {
+  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t a = blockIdx.y;
+  if (n >= ldt) return;
+  for (int j = 0; j < rank; ++j)
+    Bt[(a * rank + j) * ldt + n] = n < rows ? B[(a * rows + n) * rank + j] : (_Float16)0.f;
+}
+
+// Tokens grouped by adapter, in token order inside each (so the gradients'
+// sums have one order), and cut into chunks of at most kGradChunk tokens of
+// one adapter.  One workgroup per adapter: it counts every adapter's tokens
+// (integer LDS atomics), finds its own places and writes its own tokens.
+__global__ __launch_bounds__(1024) void group_tokens_kernel(const int* __restrict__ index,
+                                                            int64_t m, int count, int max_chunks,
+                                                            int* __restrict__ list,
+                                                            GradChunk* __restrict__ chunks,
+                                                            int2* __restrict__ ranges) {
+  __shared__ int hist[kMaxGradAdapters];
+  __shared__ int wsum[16], base[2];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int a = blockIdx.x;
+  for (int i = tid; i < count; i += 1024) hist[i] = 0;
+  __syncthreads();
+  for (int64_t t = tid; t < m; t += 1024) {
+    const int d = valid_id(index, t, count);
+    if (d >= 0) atomicAdd(&hist[d], 1);
+  }
+  __syncthreads();
+  if (wave == 0) {  // tokens and chunks of the adapters before this one
+    int tokens = 0, before = 0, total = 0;
+    for (int i = lane; i < count; i += 64) {
+      const int c = (hist[i] + kGradChunk - 1) / kGradChunk;
+      total += c;
+      if (i < a) {
+        tokens += hist[i];
+        before += c;
+      }
+    }
+    for (int o = 32; o > 0; o >>= 1) {
+      tokens += __shfl_xor(tokens, o, 64);
+      before += __shfl_xor(before, o, 64);
+      total += __shfl_xor(total, o, 64);
+    }
+    const int mine = (hist[a] + kGradChunk - 1) / kGradChunk;
+    if (lane == 0) {
+      base[0] = tokens;
+      ranges[a] = make_int2(before, mine);
+    }
+    for (int c = lane; c < mine; c += 64)
+      chunks[before + c] = GradChunk{a, tokens + c * kGradChunk,
+                                     min(kGradChunk, hist[a] - c * kGradChunk)};
+    if (a == 0)
+      for (int c = total + lane; c < max_chunks; c += 64) chunks[c] = GradChunk{-1, 0, 0};
+  }
+  __syncthreads();
+  int at = base[0];
+  for (int64_t t0 = 0; t0 < m; t0 += 1024) {
+    const int64_t t = t0 + tid;
+    const bool mine = t < m && valid_id(index, t, count) == a;
+    const unsigned long long b = __ballot(mine);
+    if (lane == 0) wsum[wave] = __popcll(b);
+    __syncthreads();
+    int pre = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      if (w < wave) pre += wsum[w];
+      all += wsum[w];
+    }
+    if (mine) list[at + pre + __popcll(b & ((1ull << lane) - 1))] = (int)t;
+    at += all;
+    __syncthreads();
+  }
+}
+
+// One chunk's sum_t left[t][j] right[t][c] for 64 j x 512 c per workgroup, on
+// v_mfma_f32_16x16x4_f32: lane (li, kg) brings token kg of four, left's
+// column 16 b + li and eight of right's columns, 8 li .. 8 li + 7 (their
+// order inside a tile is free).
+template <bool VEC, int NB>
+__global__ __launch_bounds__(256) void grad_chunk_kernel(GradJob g0, GradJob g1,
+                                                         const int* __restrict__ list,
+                                                         const GradChunk* __restrict__ chunks,
+                                                         int ldv, int rank, int jblocks) {
+  const GradJob& job = blockIdx.z < (unsigned)jblocks ? g0 : g1;
+  const int jb = (blockIdx.z % jblocks) * NB;
+  const GradChunk ch = chunks[blockIdx.y];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, kg = lane >> 4;
+  const int64_t c0 = (int64_t)blockIdx.x * 512 + 128 * wave + 8 * li;
+  if (ch.adapter < 0 || (int64_t)blockIdx.x * 512 + 128 * wave >= job.N) return;
+  f32x4 acc[NB][8];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[b][e] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int k = 0; k < ch.count; k += 4) {
+    const bool in = k + kg < ch.count;
+    const int64_t t = list[ch.begin + min(k + kg, ch.count - 1)];
+    half8 r = {};
+    if (in) r = load8<VEC>(job.right + t * job.ldr, c0, job.N);
+    float l[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) l[b] = in && 16 * (jb + b) < ldv ? job.left[t * ldv + 16 * (jb + b) + li] : 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        acc[b][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(l[b], (float)r[e], acc[b][e], 0, 0, 0);
+  }
+  float* out = job.part + (int64_t)blockIdx.y * rank * job.N;
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = 16 * (jb + b) + 4 * kg + i;
+      if (j >= rank) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c0 + e < job.N) out[j * job.N + c0 + e] = acc[b][e][i];
+    }
+}
+
+// The chunks of an adapter added in order.  out[a][j][c] (js = N, cs = 1) or
+// out[a][c][j] (js = 1, cs = rank).
+__global__ __launch_bounds__(256) void grad_reduce_kernel(GradJob g0, GradJob g1,
+                                                          const int2* __restrict__ ranges,
+                                                          int rank) {
+  const GradJob& job = blockIdx.z == 0 ? g0 : g1;
+  const int a = blockIdx.y;
+  const int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (o >= job.N * rank) return;
+  const int2 r = ranges[a];
+  float sum = 0.f;
+  for (int c = 0; c < r.y; ++c) sum += job.part[(int64_t)(r.x + c) * rank * job.N + o];
+  const int64_t j = o / job.N, n = o % job.N;
+  job.out[a * job.N * rank + j * job.js + n * job.cs] = sum;
+}
+
+__global__ __launch_bounds__(256) void fill_zero_kernel(float* p, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) p[i] = 0.f;
+}
+
+bool vec_ok(const void* p, int64_t ld, int64_t K) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0 && K % 8 == 0;
+}
+
+bool vec_job(const ShrinkJob& j) { return vec_ok(j.x, j.ldx, j.K) && vec_ok(j.down, j.ldd, j.K); }
+
+template <bool VEC, int NB>
+void shrink_tiles(const ShrinkJob& j0, const ShrinkJob* j1, int64_t m, hipStream_t s) {
+  hipLaunchKernelGGL((shrink_tile_kernel<VEC, NB>), dim3((unsigned)ceil_div(m, 16), j1 ? 2 : 1),
+                     dim3(256), 0, s, j0, j1 ? *j1 : j0, m);
+}
+
+}  // namespace
+
+hipError_t launch_shrink_rows(const ShrinkJob& job, int64_t m, hipStream_t s) {
+  const dim3 grid((unsigned)m, (unsigned)(job.ldv / 4));
+  if (vec_job(job))
+    hipLaunchKernelGGL(shrink_rows_kernel<true>, grid, dim3(256), 0, s, job, m);
+  else
+    hipLaunchKernelGGL(shrink_rows_kernel<false>, grid, dim3(256), 0, s, job, m);
+  return hipGetLastError();
+}
+
+hipError_t launch_shrink_tiles(const ShrinkJob& j0, const ShrinkJob* j1, int64_t m, hipStream_t s) {
+  const bool vec = vec_job(j0) && (j1 == nullptr || vec_job(*j1));
+  const int nb = j0.ldv / 16;
+#define GPTQ_SHRINK(V)                        \
+  if (nb == 1) shrink_tiles<V, 1>(j0, j1, m, s);      \
+  else if (nb == 2) shrink_tiles<V, 2>(j0, j1, m, s); \
+  else if (nb <= 4) shrink_tiles<V, 4>(j0, j1, m, s); \
+  else shrink_tiles<V, 8>(j0, j1, m, s);
+  if (vec) {
+    GPTQ_SHRINK(true)
+  } else {
+    GPTQ_SHRINK(false)
+  }
+#undef GPTQ_SHRINK
+  return hipGetLastError();
+}
+
+hipError_t launch_transpose_up(const _Float16* B, int64_t count, int64_t rows, int rank,
+                               int64_t ldt, _Float16* Bt, hipStream_t s) {
+  hipLaunchKernelGGL(transpose_up_kernel, dim3((unsigned)ceil_div(ldt, 256), (unsigned)count),
+                     dim3(256), 0, s, B, rows, rank, ldt, Bt);
+  return hipGetLastError();
+}
+
+int64_t grad_chunks(int64_t m, int64_t count) { return ceil_div(m, kGradChunk) + count; }
+
+hipError_t launch_group_tokens(const int* index, int64_t m, int64_t count, int* list,
+                               GradChunk* chunks, int2* ranges, hipStream_t s) {
+  hipLaunchKernelGGL(group_tokens_kernel, dim3((unsigned)count), dim3(1024), 0, s, index, m,
+                     (int)count, (int)grad_chunks(m, count), list, chunks, ranges);
+  return hipGetLastError();
+}
+
+hipError_t launch_grads(const GradJob& g0, const GradJob& g1, int64_t m, int64_t count, int rank,
+                        int ldv, const int* list, const GradChunk* chunks, const int2* ranges,
+                        hipStream_t s) {
+  const int64_t N = g0.N > g1.N ? g0.N : g1.N;
+  const bool vec = vec_ok(g0.right, g0.ldr, g0.N) && vec_ok(g1.right, g1.ldr, g1.N);
+  const int tiles = ldv / 16, nb = tiles == 1 ? 1 : tiles == 2 ? 2 : 4;
+  const int jblocks = (int)ceil_div(tiles, nb);
+  const dim3 grid((unsigned)ceil_div(N, 512), (unsigned)grad_chunks(m, count),
+                  (unsigned)(2 * jblocks));
+#define GPTQ_GRAD(V, B)                                                                    \
+  hipLaunchKernelGGL((grad_chunk_kernel<V, B>), grid, dim3(256), 0, s, g0, g1, list, chunks, \
+                     ldv, rank, jblocks)
+  if (vec) {
+    if (nb == 1) GPTQ_GRAD(true, 1);
+    else if (nb == 2) GPTQ_GRAD(true, 2);
+    else GPTQ_GRAD(true, 4);
+  } else {
+    if (nb == 1) GPTQ_GRAD(false, 1);
+    else if (nb == 2) GPTQ_GRAD(false, 2);
+    else GPTQ_GRAD(false, 4);
+  }
+#undef GPTQ_GRAD
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(grad_reduce_kernel, dim3((unsigned)ceil_div(N * rank, 256), (unsigned)count, 2),
+                     dim3(256), 0, s, g0, g1, ranges, rank);
+  return hipGetLastError();
+}
+
+hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t s) {
+  if (n == 0) return hipSuccess;
+  hipLaunchKernelGGL(fill_zero_kernel, dim3((unsigned)ceil_div(n, 256)), dim3(256), 0, s, p, n);
+  return hipGetLastError();
+}
+
+}  // namespace gptq

@@ -110,6 +110,107 @@ hipError_t launch_linear_forward(int bits, const _Float16* x, int64_t ldx, int64
                                  const uint32_t* packed, int64_t rows, int64_t cols,
                                  const float* scales, const float* zeros, int groupsize, bool relu,
                                  _Float16* y, int64_t ldy, hipStream_t s);
+// low-rank adapters
+// v[t][j] = scaling[a] * sum_k x[t][k] down[a][j][k], a = index[t] (zeros
+// where index is outside [0, count)); down rows are ldd apart
+struct ShrinkJob {
+  const _Float16* x;
+  int64_t ldx, K;
+  const _Float16* down;
+  int64_t ldd, stride;  // row and adapter strides
+  const float* scaling;
+  const int* index;
+  int count, rank;
+  float* v;
+  int ldv;
+};
+// one workgroup per token and four j (a few tokens), or 16-token tiles of one
+// or two jobs of the same ldv
+hipError_t launch_shrink_rows(const ShrinkJob& job, int64_t m, hipStream_t s);
+hipError_t launch_shrink_tiles(const ShrinkJob& j0, const ShrinkJob* j1, int64_t m, hipStream_t s);
+hipError_t launch_transpose_up(const _Float16* B, int64_t count, int64_t rows, int rank,
+                               int64_t ldt, _Float16* Bt, hipStream_t s);
+// out[a] = sum over the tokens t of adapter a of left[t][j] right[t][c]
+struct GradJob {
+  const float* left;
+  const _Float16* right;
+  int64_t ldr, N;
+  float* part;
+  float* out;
+  int64_t js, cs;
+};
+struct GradChunk {
+  int adapter, begin, count;  // adapter -1: no chunk
+};
+constexpr int kGradChunk = 256;          // tokens per partial sum
+constexpr int kMaxGradAdapters = 4096;   // token counts held in LDS
+int64_t grad_chunks(int64_t m, int64_t count);
+hipError_t launch_group_tokens(const int* index, int64_t m, int64_t count, int* list,
+                               GradChunk* chunks, int2* ranges, hipStream_t s);
+hipError_t launch_grads(const GradJob& g0, const GradJob& g1, int64_t m, int64_t count, int rank,
+                        int ldv, const int* list, const GradChunk* chunks, const int2* ranges,
+                        hipStream_t s);
+hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t s);
+constexpr int kMaxRank = 128;
+// the adapters' part of a product (adapters_dev.h)
+struct AdapterTile;
+hipError_t launch_dequant_gemv_adapters(const _Float16* x, int64_t ldx, int64_t m,
+                                        const uint32_t* packed, int bits, int64_t rows,
+                                        int64_t cols, const float* scales, const float* zeros,
+                                        int groupsize, const int* g_idx, const AdapterTile& ad,
+                                        float* y, int64_t ldy, hipStream_t s);
+hipError_t launch_linear_forward_adapters(int bits, const _Float16* x, int64_t ldx, int64_t m,
+                                          const uint32_t* packed, int64_t rows, int64_t cols,
+                                          const float* scales, const float* zeros, int groupsize,
+                                          bool relu, const AdapterTile& ad, _Float16* y,
+                                          int64_t ldy, hipStream_t s);
+// the transposed weights and the products with them
+constexpr int kKPad = 64;  // K of the fp16 product, padded with zeros
+hipError_t launch_dequant_transposed(const uint32_t* packed, int bits, int64_t rows, int64_t cols,
+                                     const float* scales, const float* zeros, int groupsize,
+                                     const int* g_idx, int64_t ldt, _Float16* Wt, hipStream_t s);
+hipError_t launch_pad_rows(const _Float16* src, int64_t lds, int64_t m, int64_t K, int64_t ldd,
+                           _Float16* dst, hipStream_t s);
+// C = A B^T, A m x K, B n x K (K % kKPad == 0, 16-byte aligned rows)
+hipError_t launch_gemm_nt_f16(const _Float16* A, int64_t lda, int64_t m, const _Float16* B,
+                              int64_t ldb, int64_t n, int64_t K, const AdapterTile* ad,
+                              _Float16* C, int64_t ldc, hipStream_t s);
+// C32 (+)= A B^T, or with C16 the finished rows: C16 = fp16(scale[t] (C32 + A B^T))
+hipError_t launch_gemm_nt_acc(const _Float16* A, int64_t lda, int64_t m, const _Float16* B,
+                              int64_t ldb, int64_t n, int64_t K, bool first, float* C32,
+                              const float* scale, _Float16* C16, int64_t ldc, hipStream_t s);
+// the vocabulary losses
+int64_t head_tiles(int bits, int64_t rows);
+// part[tile][t] = (max, sum exp(z - max)) over the tile's outputs, z = (x W_hat^T) inv_t
+hipError_t launch_head_partials(int bits, const _Float16* x, int64_t ldx, int64_t m,
+                                const uint32_t* packed, int64_t rows, int64_t cols,
+                                const float* scales, const float* zeros, int groupsize,
+                                float inv_t, float2* part, hipStream_t s);
+// P[t][r] = exp(z - lse[t]) in fp16, 0 where lse[t] is +inf and for rows <= r < ldp
+hipError_t launch_head_probs(int bits, const _Float16* x, int64_t ldx, int64_t m,
+                             const uint32_t* packed, int64_t rows, int64_t cols,
+                             const float* scales, const float* zeros, int groupsize, float inv_t,
+                             const float* lse, _Float16* P, int64_t ldp, hipStream_t s);
+// what is learnt: K entries per token, logits (their softmax) or one label
+struct HeadTargets {
+  const int* index;     // m x top
+  const float* logits;  // m x top, or NULL: one label of probability 1
+  int top;
+  float inv_t;
+};
+constexpr int kMaxTop = 256;
+hipError_t launch_head_finish(int bits, const _Float16* h, int64_t ldh, int64_t m,
+                              const uint32_t* packed, int64_t rows, int64_t cols,
+                              const float* scales, const float* zeros, int groupsize,
+                              const HeadTargets& tg, const float2* part, int64_t tiles,
+                              float* loss, float* lse, float* zk, hipStream_t s);
+// lse_eff[t] = lse[t] or +inf, gscale[t] = dloss[t] inv_t or 0 (no entries)
+hipError_t launch_head_rows(const HeadTargets& tg, int64_t m, int64_t rows, const float* lse,
+                            const float* dloss, float* lse_eff, float* gscale, hipStream_t s);
+// P[t][index - v0] = exp(zk - lse) - p for the entries inside [v0, v0 + width)
+hipError_t launch_head_scatter(const HeadTargets& tg, int64_t m, int64_t rows, int64_t v0,
+                               int64_t width, const float* zk, const float* lse, _Float16* P,
+                               int64_t ldp, hipStream_t s);
 constexpr int kSweepRows = 16;  // rows per sweep workgroup
 constexpr int kBlock = 128;     // columns per block
 constexpr int kSuperBlock = 512;  // columns per superblock of the two-level lazy update

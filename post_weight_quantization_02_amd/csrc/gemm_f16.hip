@@ -1,0 +1,250 @@
+// The gradient through a stored layer, dx = dy W_hat, and the products of the
+// vocabulary losses' gradient: the stored weights are written once in fp16
+// with the layer's outputs along the fast axis (launch_dequant_transposed),
+// and a dense fp16 product C = A B^T over that axis follows.
+//
+// W_hat = (code - zero) * scale is formed in fp32 and rounded to fp16 once
+// (at most 2^-11 of its size, 2^-25 below 2^-14); the products are exact in
+// fp32 and summed there.
+#include "adapters_dev.h"
+
+namespace gptq {
+namespace {
+
+// ------------------------------------------------------- transposed weights
+// 64 rows x 64 columns per workgroup through LDS.
+__global__ __launch_bounds__(256) void dequant_transposed_kernel(
+    const uint32_t* __restrict__ packed, int bits, int64_t nw, int64_t rows, int64_t cols,
+    const float* __restrict__ scales, const float* __restrict__ zeros, int64_t ngroups,
+    int groupsize, const int* __restrict__ g_idx, int64_t ldt, _Float16* __restrict__ Wt) {
+  __shared__ __attribute__((aligned(16))) _Float16 tile[64][64 + 8];
+  const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
+  const int tid = threadIdx.x, k = 32 / bits;
+  const uint32_t mask = (1u << bits) - 1u;
+  {
+    const int64_t c = c0 + (tid & 63);
+    const int64_t cc = c < cols ? c : cols - 1;
+    int64_t g = g_idx != nullptr ? (int64_t)g_idx[cc] : cc / groupsize;
+    g = g < 0 ? 0 : g >= ngroups ? ngroups - 1 : g;
+    const int64_t w = cc / k;
+    const int sh = bits * (int)(cc % k);
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+      const int row = (tid >> 6) * 16 + i;
+      const int64_t r = r0 + row;
+      float v = 0.f;
+      if (r < rows && c < cols) {
+        const float q = (float)((packed[r * nw + w] >> sh) & mask);
+        v = (q - zeros[r * ngroups + g]) * scales[r * ngroups + g];
+      }
+      tile[tid & 63][row] = (_Float16)v;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int o = tid + 256 * u, c = o >> 3, p = o & 7;
+    if (c0 + c < cols)
+      *reinterpret_cast<uint4*>(Wt + (c0 + c) * ldt + r0 + 8 * p) =
+          *reinterpret_cast<const uint4*>(&tile[c][8 * p]);
+  }
+}
+
+// dst[t][0 .. ldd) = src[t][0 .. K) and zeros
+__global__ __launch_bounds__(256) void pad_rows_kernel(const _Float16* __restrict__ src,
+                                                       int64_t lds, int64_t K, int64_t ldd,
+                                                       _Float16* __restrict__ dst) {
+  const int64_t t = blockIdx.x, c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
+  if (c >= ldd) return;
+  half8 v;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = c + e < K ? src[t * lds + c + e] : (_Float16)0.f;
+  *reinterpret_cast<half8*>(dst + t * ldd + c) = v;
+}
+
+// ------------------------------------------------------------ C = A B^T
+// (32 AT) x (32 BT) outputs per workgroup of four waves, each a quadrant of
+// AT x BT tiles of v_mfma_f32_16x16x32_f16.  32 columns of K of both operands
+// go straight into a 4-stage LDS ring by global_load_lds_dwordx4; a row of a
+// stage is 64 bytes, its four 16-byte pieces permuted by (row >> 2) & 3 so
+// the 16 rows a fragment read touches use 16 distinct bank groups.  Rows past
+// the operands are read clamped and not stored.
+constexpr int KC = 32;
+constexpr int NST = 4;
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+template <int N>
+__device__ inline void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+__device__ inline void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+struct GemmOut {
+  AdapterTile ad;        // kStore with adapters
+  _Float16* c16;
+  int64_t ldc;
+  float* c32;            // m x n
+  const float* scale;
+  bool first;
+};
+
+enum GemmMode { kStore = 0, kStoreAdapters = 1, kAccumulate = 2, kFinish = 3 };
+
+template <int AT, int BT, int MODE>
+__global__ __launch_bounds__(256, 1) void gemm_nt_kernel(const _Float16* __restrict__ A,
+                                                         int64_t lda, int64_t m,
+                                                         const _Float16* __restrict__ B,
+                                                         int64_t ldb, int64_t n, int64_t K,
+                                                         int64_t ntn, GemmOut o) {
+  constexpr int TM = 32 * AT, TN = 32 * BT;
+  constexpr int ABYTES = TM * KC * 2, STAGE = (TM + TN) * KC * 2;
+  constexpr int AU = TM / 64, BU = TN / 64;  // 16-row loads per wave and stage
+  constexpr int LPS = AU + BU;
+  __shared__ __attribute__((aligned(1024))) char ring[NST * STAGE];
+  const int64_t tm = blockIdx.x / ntn, tn = blockIdx.x % ntn;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1, li = lane & 15, kg = lane >> 4;
+  const int64_t t0 = tm * TM, n0 = tn * TN;
+
+  const _Float16* asrc[AU];
+  const _Float16* bsrc[BU];
+#pragma unroll
+  for (int u = 0; u < AU; ++u) {
+    const int row = 16 * (wave + 4 * u) + (lane >> 2);
+    asrc[u] = A + min(t0 + row, m - 1) * lda + 8 * ((lane & 3) ^ ((row >> 2) & 3));
+  }
+#pragma unroll
+  for (int u = 0; u < BU; ++u) {
+    const int row = 16 * (wave + 4 * u) + (lane >> 2);
+    bsrc[u] = B + min(n0 + row, n - 1) * ldb + 8 * ((lane & 3) ^ ((row >> 2) & 3));
+  }
+  auto issue = [&](int64_t k) {
+    char* st = ring + (int)(k % NST) * STAGE;
+#pragma unroll
+    for (int u = 0; u < AU; ++u)
+      __builtin_amdgcn_global_load_lds((const void*)(asrc[u] + k * KC),
+                                       (lds_void*)(st + 1024 * (wave + 4 * u)), 16, 0, 0);
+#pragma unroll
+    for (int u = 0; u < BU; ++u)
+      __builtin_amdgcn_global_load_lds((const void*)(bsrc[u] + k * KC),
+                                       (lds_void*)(st + ABYTES + 1024 * (wave + 4 * u)), 16, 0, 0);
+  };
+  f32x4 acc[AT][BT];
+#pragma unroll
+  for (int a = 0; a < AT; ++a)
+#pragma unroll
+    for (int b = 0; b < BT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int64_t nk = K / KC;
+  for (int64_t k = 0; k < NST - 1 && k < nk; ++k) issue(k);
+  const int frag = 64 * li + 16 * (kg ^ ((li >> 2) & 3));
+  for (int64_t k = 0; k < nk; ++k) {
+    if (k + 2 < nk) wait_vm<2 * LPS>();
+    else if (k + 1 < nk) wait_vm<LPS>();
+    else wait_vm<0>();
+    lds_barrier();
+    if (k + NST - 1 < nk) issue(k + NST - 1);
+    const char* as = ring + (int)(k % NST) * STAGE + wm * 16 * AT * 64 + frag;
+    const char* bs = ring + (int)(k % NST) * STAGE + ABYTES + wn * 16 * BT * 64 + frag;
+    half8 bf[BT];
+#pragma unroll
+    for (int b = 0; b < BT; ++b) bf[b] = *reinterpret_cast<const half8*>(bs + 1024 * b);
+#pragma unroll
+    for (int a = 0; a < AT; ++a) {
+      const half8 af = *reinterpret_cast<const half8*>(as + 1024 * a);
+#pragma unroll
+      for (int b = 0; b < BT; ++b)
+        acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(af, bf[b], acc[a][b], 0, 0, 0);
+    }
+  }
+
+  const int64_t tw = t0 + 16 * AT * wm, nw = n0 + 16 * BT * wn;  // this wave's corner
+  if constexpr (MODE == kStoreAdapters) add_adapters<AT, BT>(acc, o.ad, tw, m, nw, n);
+#pragma unroll
+  for (int a = 0; a < AT; ++a)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = tw + 16 * a + 4 * kg + i;
+      if (t >= m) continue;
+      const float scale = MODE == kFinish ? o.scale[t] : 1.f;
+#pragma unroll
+      for (int b = 0; b < BT; ++b) {
+        const int64_t c = nw + 16 * b + li;
+        if (c >= n) continue;
+        float v = acc[a][b][i];
+        if constexpr (MODE == kAccumulate || MODE == kFinish)
+          if (!o.first) v += o.c32[t * n + c];
+        if constexpr (MODE == kAccumulate) o.c32[t * n + c] = v;
+        else o.c16[t * o.ldc + c] = (_Float16)(MODE == kFinish ? scale * v : v);
+      }
+    }
+}
+
+template <int MODE>
+hipError_t launch_gemm(const _Float16* A, int64_t lda, int64_t m, const _Float16* B, int64_t ldb,
+                       int64_t n, int64_t K, const GemmOut& o, hipStream_t s) {
+  // 256 x 256 tiles when they fill the CUs, else 128 x 128
+  if (ceil_div(m, 256) * ceil_div(n, 256) >= 192) {
+    const int64_t ntn = ceil_div(n, 256);
+    hipLaunchKernelGGL((gemm_nt_kernel<8, 8, MODE>), dim3((unsigned)(ceil_div(m, 256) * ntn)),
+                       dim3(256), 0, s, A, lda, m, B, ldb, n, K, ntn, o);
+  } else {
+    const int64_t ntn = ceil_div(n, 128);
+    hipLaunchKernelGGL((gemm_nt_kernel<4, 4, MODE>), dim3((unsigned)(ceil_div(m, 128) * ntn)),
+                       dim3(256), 0, s, A, lda, m, B, ldb, n, K, ntn, o);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_dequant_transposed(const uint32_t* packed, int bits, int64_t rows, int64_t cols,
+                                     const float* scales, const float* zeros, int groupsize,
+                                     const int* g_idx, int64_t ldt, _Float16* Wt, hipStream_t s) {
+  hipLaunchKernelGGL(dequant_transposed_kernel,
+                     dim3((unsigned)(ldt / 64), (unsigned)ceil_div(cols, 64)), dim3(256), 0, s,
+                     packed, bits, packed_words(cols, bits), rows, cols, scales, zeros,
+                     ceil_div(cols, groupsize), groupsize, g_idx, ldt, Wt);
+  return hipGetLastError();
+}
+
+hipError_t launch_pad_rows(const _Float16* src, int64_t lds, int64_t m, int64_t K, int64_t ldd,
+                           _Float16* dst, hipStream_t s) {
+  hipLaunchKernelGGL(pad_rows_kernel, dim3((unsigned)m, (unsigned)ceil_div(ldd, 2048)), dim3(256),
+                     0, s, src, lds, K, ldd, dst);
+  return hipGetLastError();
+}
+
+hipError_t launch_gemm_nt_f16(const _Float16* A, int64_t lda, int64_t m, const _Float16* B,
+                              int64_t ldb, int64_t n, int64_t K, const AdapterTile* ad,
+                              _Float16* C, int64_t ldc, hipStream_t s) {
+  GemmOut o{};
+  o.c16 = C;
+  o.ldc = ldc;
+  if (ad == nullptr) return launch_gemm<kStore>(A, lda, m, B, ldb, n, K, o, s);
+  o.ad = *ad;
+  return launch_gemm<kStoreAdapters>(A, lda, m, B, ldb, n, K, o, s);
+}
+
+hipError_t launch_gemm_nt_acc(const _Float16* A, int64_t lda, int64_t m, const _Float16* B,
+                              int64_t ldb, int64_t n, int64_t K, bool first, float* C32,
+                              const float* scale, _Float16* C16, int64_t ldc, hipStream_t s) {
+  GemmOut o{};
+  o.c16 = C16;
+  o.ldc = ldc;
+  o.c32 = C32;
+  o.scale = scale;
+  o.first = first;
+  if (C16 == nullptr) return launch_gemm<kAccumulate>(A, lda, m, B, ldb, n, K, o, s);
+  return launch_gemm<kFinish>(A, lda, m, B, ldb, n, K, o, s);
+}
+
+}  // namespace gptq

@@ -23,7 +23,7 @@
 // are added by lane shuffles.  For 2 to 32 tokens with 4-bit codes in groups
 // of a multiple of 128 columns, the MFMA kernel reads each packed word once
 // for all of the pass's tokens (see dequant_gemm_mfma_kernel).
-#include "common.h"
+#include "adapters_dev.h"
 
 namespace gptq {
 namespace {
@@ -47,16 +47,39 @@ __global__ __launch_bounds__(256) void pack_codes_kernel(const uint8_t* __restri
   out[r * nw + w] = v;
 }
 
+// One lane's share of sum_j v[t][j] up[a][j][r], a = index[t] (the 64 lanes'
+// shares add up to it); 0 for a token without an adapter.
+__device__ inline float adapter_share(const AdapterTile& ad, int64_t t, int64_t r, int lane) {
+  const int a = ad.index[t];
+  if (a < 0 || a >= ad.count) return 0.f;
+  const _Float16* up = ad.up + a * ad.stride + r * ad.ns;
+  float sum = 0.f;
+  for (int j = lane; j < ad.rank; j += 64)
+    sum = __builtin_fmaf(ad.v[t * ad.ldv + j], (float)up[j * ad.js], sum);
+  return sum;
+}
+
+// the adapters of the tokens from t0 on
+AdapterTile from_token(const AdapterTile& ad, int64_t t0) {
+  AdapterTile b = ad;
+  if (b.v != nullptr) {
+    b.v += t0 * b.ldv;
+    b.index += t0;
+  }
+  return b;
+}
+
 constexpr int kGemvRows = 4;   // output rows per wave
 constexpr int kGemvUnroll = 4; // words per lane in flight per row
 
-// y[t][r] = sum_c x[t][c] * W_hat[r][c] for t < m <= MT.
-template <int BITS, int MT>
+// y[t][r] = sum_c x[t][c] * W_hat[r][c] for t < m <= MT (AD: plus the
+// tokens' adapters).
+template <int BITS, int MT, bool AD>
 __global__ __launch_bounds__(256) void dequant_gemv_kernel(
     const _Float16* __restrict__ x, int64_t ldx, int m, const uint32_t* __restrict__ packed,
     int64_t nw, int64_t rows, int64_t cols, const float* __restrict__ scales,
     const float* __restrict__ zeros, int64_t ngroups, int groupsize, const int* __restrict__ g_idx,
-    float* __restrict__ y, int64_t ldy) {
+    float* __restrict__ y, int64_t ldy, AdapterTile ad) {
   constexpr int K = 32 / BITS;
   constexpr uint32_t MASK = (1u << BITS) - 1u;
   constexpr int R = kGemvRows;
@@ -127,6 +150,13 @@ __global__ __launch_bounds__(256) void dequant_gemv_kernel(
       }
     }
   }
+  if constexpr (AD) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        if (t < m) acc[i][t] += adapter_share(ad, t, rr[i], lane);
+  }
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -173,12 +203,12 @@ __device__ inline void unpack_word(uint32_t w, float (&q)[32 / BITS]) {
 // equals sum x (q - z) s.  Rounding: the products x * q are exact in fp32,
 // so each output's error is at most
 // (4K + ceil(runs / 64) + 8) * 2^-24 * sum_c |x_c| (|q_c| + |z_g|) s_g.
-template <int BITS, int MT, int R, bool XD>
+template <int BITS, int MT, int R, bool XD, bool AD>
 __global__ __launch_bounds__(256) void dequant_gemv_fast_kernel(
     const _Float16* __restrict__ x, int64_t ldx, int m, const uint32_t* __restrict__ packed,
     int64_t nw, int64_t rows, int64_t cols, const float* __restrict__ scales,
     const float* __restrict__ zeros, int64_t ngroups, int groupsize, float* __restrict__ y,
-    int64_t ldy, bool xvec) {
+    int64_t ldy, bool xvec, AdapterTile ad) {
   constexpr int K = 32 / BITS;
   constexpr int CW = 4 * K;  // columns per 4-word run
   // R: output rows per wave.  XD (4 bits, one token, cols a multiple of 32,
@@ -368,6 +398,13 @@ __global__ __launch_bounds__(256) void dequant_gemv_fast_kernel(
       }
     }
   }
+  if constexpr (AD) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        if (t < m) acc[i][t] += adapter_share(ad, t, rr[i], lane);
+  }
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -429,12 +466,12 @@ __device__ inline half8 codes4_f16(uint32_t w) {
   return r;
 }
 
-template <int TT>  // token tiles of 16 per pass
+template <int TT, bool AD>  // token tiles of 16 per pass
 __global__ __launch_bounds__(256) void dequant_gemm_mfma_kernel(
     const _Float16* __restrict__ x, int64_t ldx, int m, const uint32_t* __restrict__ packed,
     int64_t nw, int64_t rows, int64_t cols, const float* __restrict__ scales,
     const float* __restrict__ zeros, int64_t ngroups, int groupsize, float* __restrict__ y,
-    int64_t ldy) {
+    int64_t ldy, AdapterTile ad) {
   __shared__ float part[4][TT * 16][17];  // per-wave partial tiles [wave][token][row]
   const int tid = threadIdx.x;
   const int lane = tid & 63, wave = tid >> 6;
@@ -514,7 +551,19 @@ __global__ __launch_bounds__(256) void dequant_gemm_mfma_kernel(
   __syncthreads();
   for (int o = tid; o < TT * 256; o += 256) {
     const int tok = o >> 4, rw = o & 15;
-    const float v = (part[0][tok][rw] + part[1][tok][rw]) + (part[2][tok][rw] + part[3][tok][rw]);
+    float v = (part[0][tok][rw] + part[1][tok][rw]) + (part[2][tok][rw] + part[3][tok][rw]);
+    if constexpr (AD) {
+      if (tok < m && r0 + rw < rows) {
+        const int a = ad.index[tok];
+        if (a >= 0 && a < ad.count) {
+          const _Float16* up = ad.up + a * ad.stride + (r0 + rw) * ad.ns;
+          float low = 0.f;
+          for (int j = 0; j < ad.rank; ++j)
+            low = __builtin_fmaf(ad.v[(int64_t)tok * ad.ldv + j], (float)up[j * ad.js], low);
+          v += low;
+        }
+      }
+    }
     if (tok < m && r0 + rw < rows) y[(int64_t)tok * ldy + r0 + rw] = v;
   }
 }
@@ -527,23 +576,24 @@ bool dequant_mfma_ok(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* 
          (reinterpret_cast<uintptr_t>(packed) & 15) == 0;
 }
 
+template <bool AD>
 hipError_t launch_dequant_mfma(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed,
                                int64_t rows, int64_t cols, const float* scales,
-                               const float* zeros, int groupsize, float* y, int64_t ldy,
-                               hipStream_t s) {
+                               const float* zeros, int groupsize, const AdapterTile& ad, float* y,
+                               int64_t ldy, hipStream_t s) {
   const int64_t nw = packed_words(cols, 4);
   const int64_t ngroups = ceil_div(cols, groupsize);
   const dim3 grid((unsigned)ceil_div(rows, 16));
   for (int64_t t0 = 0; t0 < m; t0 += 32) {
     const int mt = (int)((m - t0 < 32) ? m - t0 : 32);
     if (mt > 16)
-      hipLaunchKernelGGL(dequant_gemm_mfma_kernel<2>, grid, dim3(256), 0, s, x + t0 * ldx, ldx, mt,
+      hipLaunchKernelGGL((dequant_gemm_mfma_kernel<2, AD>), grid, dim3(256), 0, s, x + t0 * ldx, ldx, mt,
                          packed, nw, rows, cols, scales, zeros, ngroups, groupsize, y + t0 * ldy,
-                         ldy);
+                         ldy, from_token(ad, t0));
     else
-      hipLaunchKernelGGL(dequant_gemm_mfma_kernel<1>, grid, dim3(256), 0, s, x + t0 * ldx, ldx, mt,
+      hipLaunchKernelGGL((dequant_gemm_mfma_kernel<1, AD>), grid, dim3(256), 0, s, x + t0 * ldx, ldx, mt,
                          packed, nw, rows, cols, scales, zeros, ngroups, groupsize, y + t0 * ldy,
-                         ldy);
+                         ldy, from_token(ad, t0));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -552,27 +602,29 @@ hipError_t launch_dequant_mfma(const _Float16* x, int64_t ldx, int64_t m, const 
 
 constexpr int64_t kGemvLds = 64 * 1024;  // x staging limit of the fast path
 
-template <int BITS, int R>
+template <int BITS, int R, bool AD>
 hipError_t launch_gemv_fast_direct(const _Float16* x, int64_t ldx, int64_t m,
                                    const uint32_t* packed, int64_t nw, int64_t rows, int64_t cols,
                                    const float* scales, const float* zeros, int64_t ngroups,
-                                   int groupsize, float* y, int64_t ldy, hipStream_t s) {
+                                   int groupsize, const AdapterTile& ad, float* y, int64_t ldy,
+                                   hipStream_t s) {
   const dim3 grid((unsigned)ceil_div(rows, 4 * R));
   for (int64_t t0 = 0; t0 < m; ++t0) {
-    hipLaunchKernelGGL((dequant_gemv_fast_kernel<BITS, 1, R, true>), grid, dim3(256), 0, s,
+    hipLaunchKernelGGL((dequant_gemv_fast_kernel<BITS, 1, R, true, AD>), grid, dim3(256), 0, s,
                        x + t0 * ldx, ldx, 1, packed, nw, rows, cols, scales, zeros, ngroups,
-                       groupsize, y + t0 * ldy, ldy, true);
+                       groupsize, y + t0 * ldy, ldy, true, from_token(ad, t0));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-template <int BITS, int R>
+template <int BITS, int R, bool AD>
 hipError_t launch_gemv_fast(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed,
                             int64_t nw, int64_t rows, int64_t cols, const float* scales,
-                            const float* zeros, int64_t ngroups, int groupsize, float* y,
-                            int64_t ldy, int maxmt, hipStream_t s) {
+                            const float* zeros, int64_t ngroups, int groupsize,
+                            const AdapterTile& ad, float* y, int64_t ldy, int maxmt,
+                            hipStream_t s) {
   const dim3 grid((unsigned)ceil_div(rows, 4 * R));
   const int64_t row_bytes = nw * (32 / BITS) * 2;
   const bool xvec = (ldx % 8 == 0) && ((reinterpret_cast<uintptr_t>(x) & 15) == 0);
@@ -581,46 +633,103 @@ hipError_t launch_gemv_fast(const _Float16* x, int64_t ldx, int64_t m, const uin
     const _Float16* xt = x + t0 * ldx;
     float* yt = y + t0 * ldy;
     if (mt == 1)
-      hipLaunchKernelGGL((dequant_gemv_fast_kernel<BITS, 1, R, false>), grid, dim3(256),
+      hipLaunchKernelGGL((dequant_gemv_fast_kernel<BITS, 1, R, false, AD>), grid, dim3(256),
                          (unsigned)row_bytes, s, xt, ldx, mt, packed, nw, rows, cols, scales,
-                         zeros, ngroups, groupsize, yt, ldy, xvec);
+                         zeros, ngroups, groupsize, yt, ldy, xvec, from_token(ad, t0));
     else if (mt == 2)
-      hipLaunchKernelGGL((dequant_gemv_fast_kernel<BITS, 2, R, false>), grid, dim3(256),
+      hipLaunchKernelGGL((dequant_gemv_fast_kernel<BITS, 2, R, false, AD>), grid, dim3(256),
                          (unsigned)(2 * row_bytes), s, xt, ldx, mt, packed, nw, rows, cols,
-                         scales, zeros, ngroups, groupsize, yt, ldy, xvec);
+                         scales, zeros, ngroups, groupsize, yt, ldy, xvec, from_token(ad, t0));
     else
-      hipLaunchKernelGGL((dequant_gemv_fast_kernel<BITS, 4, R, false>), grid, dim3(256),
+      hipLaunchKernelGGL((dequant_gemv_fast_kernel<BITS, 4, R, false, AD>), grid, dim3(256),
                          (unsigned)(4 * row_bytes), s, xt, ldx, mt, packed, nw, rows, cols,
-                         scales, zeros, ngroups, groupsize, yt, ldy, xvec);
+                         scales, zeros, ngroups, groupsize, yt, ldy, xvec, from_token(ad, t0));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-template <int BITS>
+template <int BITS, bool AD>
 hipError_t launch_gemv_bits(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed,
                             int64_t nw, int64_t rows, int64_t cols, const float* scales,
                             const float* zeros, int64_t ngroups, int groupsize, const int* g_idx,
-                            float* y, int64_t ldy, hipStream_t s) {
+                            const AdapterTile& ad, float* y, int64_t ldy, hipStream_t s) {
   const dim3 grid((unsigned)ceil_div(rows, 4 * kGemvRows));
   for (int64_t t0 = 0; t0 < m; t0 += 4) {
     const int mt = (int)((m - t0 < 4) ? m - t0 : 4);
     const _Float16* xt = x + t0 * ldx;
     float* yt = y + t0 * ldy;
     if (mt == 1)
-      hipLaunchKernelGGL((dequant_gemv_kernel<BITS, 1>), grid, dim3(256), 0, s, xt, ldx, mt,
-                         packed, nw, rows, cols, scales, zeros, ngroups, groupsize, g_idx, yt, ldy);
+      hipLaunchKernelGGL((dequant_gemv_kernel<BITS, 1, AD>), grid, dim3(256), 0, s, xt, ldx, mt,
+                         packed, nw, rows, cols, scales, zeros, ngroups, groupsize, g_idx, yt, ldy,
+                         from_token(ad, t0));
     else if (mt == 2)
-      hipLaunchKernelGGL((dequant_gemv_kernel<BITS, 2>), grid, dim3(256), 0, s, xt, ldx, mt,
-                         packed, nw, rows, cols, scales, zeros, ngroups, groupsize, g_idx, yt, ldy);
+      hipLaunchKernelGGL((dequant_gemv_kernel<BITS, 2, AD>), grid, dim3(256), 0, s, xt, ldx, mt,
+                         packed, nw, rows, cols, scales, zeros, ngroups, groupsize, g_idx, yt, ldy,
+                         from_token(ad, t0));
     else
-      hipLaunchKernelGGL((dequant_gemv_kernel<BITS, 4>), grid, dim3(256), 0, s, xt, ldx, mt,
-                         packed, nw, rows, cols, scales, zeros, ngroups, groupsize, g_idx, yt, ldy);
+      hipLaunchKernelGGL((dequant_gemv_kernel<BITS, 4, AD>), grid, dim3(256), 0, s, xt, ldx, mt,
+                         packed, nw, rows, cols, scales, zeros, ngroups, groupsize, g_idx, yt, ldy,
+                         from_token(ad, t0));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+// (AD false: ad is not read)
+template <bool AD>
+hipError_t launch_gemv_any(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed,
+                           int bits, int64_t rows, int64_t cols, const float* scales,
+                           const float* zeros, int groupsize, const int* g_idx,
+                           const AdapterTile& ad, float* y, int64_t ldy, hipStream_t s) {
+  const int64_t nw = packed_words(cols, bits);
+  const int64_t ngroups = ceil_div(cols, groupsize);
+  // two tokens or more, 4 bits, whole 128-column chunks inside groups: MFMA,
+  // the weights read once per 32 tokens
+  if (dequant_mfma_ok(x, ldx, m, packed, bits, cols, groupsize, g_idx))
+    return launch_dequant_mfma<AD>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize, ad, y, ldy,
+                                   s);
+  // fast path: 2, 4 or 8 bits, whole 4-word runs inside groups, no g_idx,
+  // 16-byte aligned rows, x of at least one token fits the LDS staging
+  if ((bits == 2 || bits == 4 || bits == 8) && g_idx == nullptr && nw % 4 == 0 &&
+      groupsize % (4 * (32 / bits)) == 0 && (reinterpret_cast<uintptr_t>(packed) & 15) == 0) {
+    const int64_t row_bytes = nw * (32 / bits) * 2;
+    const int maxmt = (int)((kGemvLds / row_bytes >= 4) ? 4 : (kGemvLds / row_bytes >= 2) ? 2
+                                                                                          : 1);
+    if (row_bytes <= kGemvLds) {
+      // two rows per wave (measured against one and four: 1.78 ms per
+      // decode step against 1.86 and 1.81 at one token)
+      if (bits == 2)
+        return launch_gemv_fast<2, 2, AD>(x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups,
+                                      groupsize, ad, y, ldy, maxmt, s);
+      // one token, whole 32-column runs, aligned x rows: x loaded directly
+      if (bits == 4 && m == 1 && cols % 32 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0)
+        return launch_gemv_fast_direct<4, 2, AD>(x, ldx, m, packed, nw, rows, cols, scales, zeros,
+                                             ngroups, groupsize, ad, y, ldy, s);
+      if (bits == 4)
+        return launch_gemv_fast<4, 2, AD>(x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups,
+                                      groupsize, ad, y, ldy, maxmt, s);
+      return launch_gemv_fast<8, 2, AD>(x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups,
+                                    groupsize, ad, y, ldy, maxmt, s);
+    }
+  }
+  switch (bits) {
+#define GPTQ_GEMV(B) \
+  case B:            \
+    return launch_gemv_bits<B, AD>(x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups, \
+                               groupsize, g_idx, ad, y, ldy, s);
+    GPTQ_GEMV(2)
+    GPTQ_GEMV(3)
+    GPTQ_GEMV(4)
+    GPTQ_GEMV(5)
+    GPTQ_GEMV(6)
+    GPTQ_GEMV(7)
+    GPTQ_GEMV(8)
+#undef GPTQ_GEMV
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace
@@ -640,51 +749,17 @@ hipError_t launch_dequant_gemv(const _Float16* x, int64_t ldx, int64_t m, const 
                                int bits, int64_t rows, int64_t cols, const float* scales,
                                const float* zeros, int groupsize, const int* g_idx, float* y,
                                int64_t ldy, hipStream_t s) {
-  const int64_t nw = packed_words(cols, bits);
-  const int64_t ngroups = ceil_div(cols, groupsize);
-  // two tokens or more, 4 bits, whole 128-column chunks inside groups: MFMA,
-  // the weights read once per 32 tokens
-  if (dequant_mfma_ok(x, ldx, m, packed, bits, cols, groupsize, g_idx))
-    return launch_dequant_mfma(x, ldx, m, packed, rows, cols, scales, zeros, groupsize, y, ldy, s);
-  // fast path: 2, 4 or 8 bits, whole 4-word runs inside groups, no g_idx,
-  // 16-byte aligned rows, x of at least one token fits the LDS staging
-  if ((bits == 2 || bits == 4 || bits == 8) && g_idx == nullptr && nw % 4 == 0 &&
-      groupsize % (4 * (32 / bits)) == 0 && (reinterpret_cast<uintptr_t>(packed) & 15) == 0) {
-    const int64_t row_bytes = nw * (32 / bits) * 2;
-    const int maxmt = (int)((kGemvLds / row_bytes >= 4) ? 4 : (kGemvLds / row_bytes >= 2) ? 2
-                                                                                          : 1);
-    if (row_bytes <= kGemvLds) {
-      // two rows per wave (measured against one and four: 1.78 ms per
-      // decode step against 1.86 and 1.81 at one token)
-      if (bits == 2)
-        return launch_gemv_fast<2, 2>(x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups,
-                                      groupsize, y, ldy, maxmt, s);
-      // one token, whole 32-column runs, aligned x rows: x loaded directly
-      if (bits == 4 && m == 1 && cols % 32 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0)
-        return launch_gemv_fast_direct<4, 2>(x, ldx, m, packed, nw, rows, cols, scales, zeros,
-                                             ngroups, groupsize, y, ldy, s);
-      if (bits == 4)
-        return launch_gemv_fast<4, 2>(x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups,
-                                      groupsize, y, ldy, maxmt, s);
-      return launch_gemv_fast<8, 2>(x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups,
-                                    groupsize, y, ldy, maxmt, s);
-    }
-  }
-  switch (bits) {
-#define GPTQ_GEMV(B) \
-  case B:            \
-    return launch_gemv_bits<B>(x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups, \
-                               groupsize, g_idx, y, ldy, s);
-    GPTQ_GEMV(2)
-    GPTQ_GEMV(3)
-    GPTQ_GEMV(4)
-    GPTQ_GEMV(5)
-    GPTQ_GEMV(6)
-    GPTQ_GEMV(7)
-    GPTQ_GEMV(8)
-#undef GPTQ_GEMV
-    default: return hipErrorInvalidValue;
-  }
+  return launch_gemv_any<false>(x, ldx, m, packed, bits, rows, cols, scales, zeros, groupsize,
+                                g_idx, AdapterTile{}, y, ldy, s);
+}
+
+hipError_t launch_dequant_gemv_adapters(const _Float16* x, int64_t ldx, int64_t m,
+                                        const uint32_t* packed, int bits, int64_t rows,
+                                        int64_t cols, const float* scales, const float* zeros,
+                                        int groupsize, const int* g_idx, const AdapterTile& ad,
+                                        float* y, int64_t ldy, hipStream_t s) {
+  return launch_gemv_any<true>(x, ldx, m, packed, bits, rows, cols, scales, zeros, groupsize,
+                               g_idx, ad, y, ldy, s);
 }
 
 }  // namespace gptq

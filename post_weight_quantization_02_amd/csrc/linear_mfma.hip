@@ -35,7 +35,7 @@
 //     (4 bits) or two (8 bits) 16-byte pieces of the packed row.
 //   * XCD-aware order: an XCD works on groups of 4 token tiles x all output
 //     tiles, 4 x 8 tiles at a time, so its L2 serves both operands.
-#include "common.h"
+#include "adapters_dev.h"
 
 namespace gptq {
 namespace {
@@ -349,12 +349,71 @@ __device__ inline void stage_step(int k, int nk, const char* cur, char* nxt, con
   }
 }
 
-template <int BITS, bool RELU>
+// What becomes of a tile's sums:
+//   kStore     fp16 outputs, the layer's own product
+//   kAdapters  the adapters' part added first (adapters_dev.h)
+//   kPartials  z = sum * inv_t: per token the tile's max and sum exp(z - max),
+//              the pieces of the softmax statistics of a vocabulary whose
+//              logits are not kept
+//   kProbs     exp(z - lse) in fp16, the softmax of one piece of it
+enum TailMode { kStore = 0, kAdapters = 1, kPartials = 2, kProbs = 3 };
+struct Tail {
+  AdapterTile ad;
+  float inv_t;
+  float2* part;      // output tiles x m
+  const float* lse;  // m
+};
+
+// (max, sum exp(z - max)) of the tile's outputs for each of its 128 tokens:
+// over the wave's outputs in registers and 16-lane shuffles, over the waves
+// through LDS.  Outputs past the matrix count as -inf.
+template <int BT>
+__device__ inline void tile_partials(const f32x4 (&acc)[AT][BT], const Tail& tail, float2* red,
+                                     int64_t t0, int64_t m, int64_t tn, int64_t nw, int64_t rows) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, kg = lane >> 4;
+  __syncthreads();  // the stages are free
+#pragma unroll
+  for (int a = 0; a < AT; ++a)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float z[BT], top = -INFINITY;
+#pragma unroll
+      for (int b = 0; b < BT; ++b) {
+        z[b] = nw + 16 * b + li < rows ? acc[a][b][i] * tail.inv_t : -INFINITY;
+        top = fmaxf(top, z[b]);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+      const float base = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+#pragma unroll
+      for (int b = 0; b < BT; ++b) sum += __expf(z[b] - base);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+      if (li == 0) red[wave * TM + 16 * a + 4 * kg + i] = make_float2(top, sum);
+    }
+  __syncthreads();
+  if (tid < TM && t0 + tid < m) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NWAVE; ++w) top = fmaxf(top, red[w * TM + tid].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < NWAVE; ++w) {
+      const float2 p = red[w * TM + tid];
+      sum += p.y * (p.x == -INFINITY ? 0.f : __expf(p.x - base));
+    }
+    tail.part[tn * m + t0 + tid] = make_float2(top, sum);
+  }
+}
+
+template <int BITS, bool RELU, int TAIL>
 __global__ __launch_bounds__(512, 1) void linear_kernel(
     const _Float16* __restrict__ x, int64_t ldx, int64_t m, const uint32_t* __restrict__ packed,
     int64_t nw, int64_t rows, int64_t cols, const float* __restrict__ scales,
     const float* __restrict__ zeros, int64_t ngroups, int gk, int64_t ntn, int64_t ntm,
-    _Float16* __restrict__ y, int64_t ldy) {
+    _Float16* __restrict__ y, int64_t ldy, Tail tail) {
   using L = Lay<BITS>;
   constexpr int BT = L::BT;
   __shared__ __attribute__((aligned(1024))) char st0[L::STAGE];
@@ -423,6 +482,14 @@ __global__ __launch_bounds__(512, 1) void linear_kernel(
   }
   fold_group<BT>(acc, part, fsc);  // the last stage always ends a group
 
+  if constexpr (TAIL == kAdapters)
+    add_adapters<AT, BT>(acc, tail.ad, t0, m, n0 + L::WTN * wave, rows);
+  if constexpr (TAIL == kPartials) {
+    tile_partials<BT>(acc, tail, reinterpret_cast<float2*>(st0), t0, m, tn, n0 + L::WTN * wave,
+                      rows);
+    return;
+  }
+
   // lane holds rows 4 * kg + i of each 16 x 16 tile, column li
 #pragma unroll
   for (int a = 0; a < AT; ++a)
@@ -430,6 +497,17 @@ __global__ __launch_bounds__(512, 1) void linear_kernel(
     for (int i = 0; i < 4; ++i) {
       const int64_t t = t0 + 16 * a + 4 * kg + i;
       if (t >= m) continue;
+      if constexpr (TAIL == kProbs) {
+        const float lse = tail.lse[t];
+#pragma unroll
+        for (int b = 0; b < BT; ++b) {
+          const int64_t r = n0 + L::WTN * wave + 16 * b + li;
+          const bool in = r < rows && lse != INFINITY;
+          const float p = in ? __expf(acc[a][b][i] * tail.inv_t - lse) : 0.f;
+          if (r < ldy) y[t * ldy + r] = (_Float16)p;
+        }
+        continue;
+      }
 #pragma unroll
       for (int b = 0; b < BT; ++b) {
         const int64_t r = n0 + L::WTN * wave + 16 * b + li;
@@ -447,25 +525,32 @@ int64_t linear_blocks(int bits, int64_t m, int64_t rows) {
   return kXcds * round_up(ceil_div(ceil_div(m, TM), kXcds), kGroupM) * ceil_div(rows, tn);
 }
 
-template <int BITS>
-hipError_t launch_bits(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed,
+template <int BITS, bool RELU, int TAIL>
+hipError_t launch_tail(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed,
                        int64_t rows, int64_t cols, const float* scales, const float* zeros,
-                       int groupsize, bool relu, _Float16* y, int64_t ldy, hipStream_t s) {
+                       int groupsize, const Tail& tail, _Float16* y, int64_t ldy, hipStream_t s) {
   const int g = groupsize >= cols ? (int)cols : groupsize;
   const int64_t ngroups = ceil_div(cols, g);
   const int gk = (int)ceil_div(g, KG);  // stages per group (a short last group ends at cols)
   const int64_t nw = cols * BITS / 32;
   const int64_t ntm = ceil_div(m, TM), ntn = ceil_div(rows, Geo<BITS>::TN);
   const int64_t blocks = linear_blocks(BITS, m, rows);
-  if (relu)
-    hipLaunchKernelGGL((linear_kernel<BITS, true>), dim3((unsigned)blocks), dim3(64 * NWAVE), 0, s,
-                       x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups, gk, ntn, ntm, y,
-                       ldy);
-  else
-    hipLaunchKernelGGL((linear_kernel<BITS, false>), dim3((unsigned)blocks), dim3(64 * NWAVE), 0,
-                       s, x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups, gk, ntn, ntm,
-                       y, ldy);
+  hipLaunchKernelGGL((linear_kernel<BITS, RELU, TAIL>), dim3((unsigned)blocks), dim3(64 * NWAVE), 0,
+                     s, x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups, gk, ntn, ntm, y,
+                     ldy, tail);
   return hipGetLastError();
+}
+
+template <int BITS, int TAIL>
+hipError_t launch_bits(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed,
+                       int64_t rows, int64_t cols, const float* scales, const float* zeros,
+                       int groupsize, bool relu, const Tail& tail, _Float16* y, int64_t ldy,
+                       hipStream_t s) {
+  if (relu)
+    return launch_tail<BITS, true, TAIL>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize,
+                                         tail, y, ldy, s);
+  return launch_tail<BITS, false, TAIL>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize,
+                                        tail, y, ldy, s);
 }
 
 }  // namespace
@@ -486,8 +571,56 @@ hipError_t launch_linear_forward(int bits, const _Float16* x, int64_t ldx, int64
                                  const float* scales, const float* zeros, int groupsize, bool relu,
                                  _Float16* y, int64_t ldy, hipStream_t s) {
   if (bits == 4)
-    return launch_bits<4>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize, relu, y, ldy, s);
-  return launch_bits<8>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize, relu, y, ldy, s);
+    return launch_bits<4, kStore>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize, relu,
+                                  Tail{}, y, ldy, s);
+  return launch_bits<8, kStore>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize, relu,
+                                Tail{}, y, ldy, s);
+}
+
+hipError_t launch_linear_forward_adapters(int bits, const _Float16* x, int64_t ldx, int64_t m,
+                                          const uint32_t* packed, int64_t rows, int64_t cols,
+                                          const float* scales, const float* zeros, int groupsize,
+                                          bool relu, const AdapterTile& ad, _Float16* y,
+                                          int64_t ldy, hipStream_t s) {
+  Tail tail{};
+  tail.ad = ad;
+  if (bits == 4)
+    return launch_bits<4, kAdapters>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize, relu,
+                                     tail, y, ldy, s);
+  return launch_bits<8, kAdapters>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize, relu,
+                                   tail, y, ldy, s);
+}
+
+int64_t head_tiles(int bits, int64_t rows) {
+  return ceil_div(rows, bits == 4 ? Geo<4>::TN : Geo<8>::TN);
+}
+
+hipError_t launch_head_partials(int bits, const _Float16* x, int64_t ldx, int64_t m,
+                                const uint32_t* packed, int64_t rows, int64_t cols,
+                                const float* scales, const float* zeros, int groupsize,
+                                float inv_t, float2* part, hipStream_t s) {
+  Tail tail{};
+  tail.inv_t = inv_t;
+  tail.part = part;
+  if (bits == 4)
+    return launch_tail<4, false, kPartials>(x, ldx, m, packed, rows, cols, scales, zeros,
+                                            groupsize, tail, nullptr, 0, s);
+  return launch_tail<8, false, kPartials>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize,
+                                          tail, nullptr, 0, s);
+}
+
+hipError_t launch_head_probs(int bits, const _Float16* x, int64_t ldx, int64_t m,
+                             const uint32_t* packed, int64_t rows, int64_t cols,
+                             const float* scales, const float* zeros, int groupsize, float inv_t,
+                             const float* lse, _Float16* P, int64_t ldp, hipStream_t s) {
+  Tail tail{};
+  tail.inv_t = inv_t;
+  tail.lse = lse;
+  if (bits == 4)
+    return launch_tail<4, false, kProbs>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize,
+                                         tail, P, ldp, s);
+  return launch_tail<8, false, kProbs>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize,
+                                       tail, P, ldp, s);
 }
 
 }  // namespace gptq

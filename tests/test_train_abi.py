@@ -1,0 +1,151 @@
+"""What the adapters', backward and vocabulary-loss entry points refuse, on the
+host before any HIP call (no compute entry point is reached)."""
+import ctypes
+
+import pytest
+
+gq = pytest.importorskip("post_weight_quantization_02_amd")
+torch = pytest.importorskip("torch")
+from post_weight_quantization_02_amd import _lib  # noqa: E402
+
+lib = gq.lib
+FAKE = 0x100000  # aligned, non-null, never dereferenced (validation fails first)
+BAD, WS, UNSUP = gq.GPTQ_ERR_INVALID_ARG, gq.GPTQ_ERR_WORKSPACE, gq.GPTQ_ERR_UNSUPPORTED
+
+
+def _ad(A=FAKE, B=FAKE, scaling=FAKE, index=FAKE, count=2, rank=8):
+    return ctypes.byref(_lib._Adapters(A, B, scaling, index, count, rank))
+
+
+def _fwd(name="linear", x=FAKE, m=4, cols=256, ldx=256, packed=FAKE, bits=4, rows=32, scales=FAKE,
+         zeros=FAKE, group=128, relu=0, ad=None, y=FAKE, ldy=32, ws=None, wsb=0):
+    ad = _ad() if ad is None else ad
+    if name == "linear":
+        return lib.gptq_linear_forward_adapters(x, m, cols, ldx, packed, bits, rows, scales, zeros,
+                                                group, relu, ad, y, ldy, ws, wsb, None)
+    return lib.gptq_dequant_gemm_adapters(x, m, cols, ldx, packed, bits, rows, scales, zeros, group,
+                                          None, ad, y, ldy, ws, wsb, None)
+
+
+BAD_SIZES = [dict(x=None), dict(y=None), dict(packed=None), dict(scales=None), dict(zeros=None),
+             dict(m=-1), dict(cols=0), dict(rows=0), dict(bits=1), dict(bits=9), dict(group=0),
+             dict(ldx=255), dict(ldy=31), dict(x=FAKE + 1), dict(packed=FAKE + 2)]
+BAD_ADAPTERS = [dict(A=None), dict(B=None), dict(scaling=None), dict(index=None), dict(count=0),
+                dict(count=2 ** 20 + 1), dict(rank=0), dict(rank=-1), dict(A=FAKE + 1),
+                dict(scaling=FAKE + 2), dict(index=FAKE + 2)]
+
+
+@pytest.mark.parametrize("name", ["linear", "decode"])
+def test_adapters_refusals(name):
+    for bad in BAD_SIZES:
+        assert _fwd(name, **bad) == BAD, bad
+    for bad in BAD_ADAPTERS:
+        assert _fwd(name, ad=_ad(**bad)) == BAD, bad
+    assert _fwd(name, ad=ctypes.POINTER(_lib._Adapters)()) == BAD
+    assert _fwd(name, ad=_ad(rank=129)) == UNSUP
+    assert _fwd(name, m=2 ** 23 + 1) == UNSUP
+    assert _fwd(name, m=0, x=None, y=None, ad=_ad(index=None)) == gq.GPTQ_OK
+    need = gq.adapters_workspace_bytes(gq.OP_FORWARD_ADAPTERS, 4, 32, 256, 2, 8)
+    assert need > 0 and _fwd(name) == WS and _fwd(name, ws=FAKE, wsb=need - 1) == WS
+    assert _fwd(name, ws=FAKE + 16, wsb=need) == BAD
+
+
+def test_linear_forward_adapters_refuses_what_linear_forward_does():
+    assert _fwd(relu=2) == BAD
+    for bad in (dict(bits=3), dict(group=64), dict(cols=200, ldx=200), dict(x=FAKE + 2),
+                dict(ldx=257), dict(packed=FAKE + 4)):
+        assert _fwd(**bad) == UNSUP, bad
+
+
+def _bwd(dy=FAKE, m=4, rows=64, lddy=64, packed=FAKE, bits=4, cols=256, scales=FAKE, zeros=FAKE,
+         group=128, ad=None, x=FAKE, ldx=256, dx=FAKE, lddx=256, dA=FAKE, dB=FAKE, ws=None, wsb=0):
+    return lib.gptq_linear_backward(dy, m, rows, lddy, packed, bits, cols, scales, zeros, group, None,
+                                    ad, x, ldx, dx, lddx, dA, dB, ws, wsb, None)
+
+
+def test_backward_refusals():
+    for bad in (dict(dy=None), dict(dx=None), dict(m=-1), dict(lddy=63), dict(lddx=255),
+                dict(bits=0), dict(group=0), dict(packed=None), dict(scales=FAKE + 1)):
+        assert _bwd(**bad) == BAD, bad
+    for bad in (dict(x=None), dict(ldx=255), dict(dA=None), dict(dB=None), dict(dA=FAKE + 2)):
+        assert _bwd(ad=_ad(), **bad) == BAD, bad
+        if "dA" not in bad and "dB" not in bad:
+            assert _bwd(**bad) == WS  # not read without adapters
+    for bad in BAD_ADAPTERS:
+        assert _bwd(ad=_ad(**bad)) == BAD, bad
+    assert _bwd(ad=_ad(rank=129)) == UNSUP
+    assert _bwd(ad=_ad(count=4097)) == UNSUP
+    assert _bwd(dy=FAKE + 2) == UNSUP       # whole 64-row runs are read 16 bytes at a time
+    assert _bwd(lddy=65) == UNSUP
+    assert _bwd(rows=63, lddy=65, dy=FAKE + 2) == WS  # other rows are copied: any alignment
+    assert _bwd(m=0, dy=None, dx=None) == gq.GPTQ_OK
+    need = gq.adapters_workspace_bytes(gq.OP_BACKWARD, 4, 64, 256, 2, 8)
+    assert _bwd(ad=_ad(), ws=FAKE, wsb=need - 1) == WS
+    assert _bwd(ad=_ad(), ws=FAKE + 128, wsb=need) == BAD
+
+
+def _loss(h=FAKE, m=4, cols=256, ldh=256, packed=FAKE, bits=4, rows=500, scales=FAKE, zeros=FAKE,
+          group=128, index=FAKE, loss=FAKE, lse=FAKE, zk=FAKE, ws=None, wsb=0, teacher=None, top=8,
+          T=1.0, dloss=FAKE, dh=FAKE, lddh=256, kind="loss"):
+    head = (h, m, cols, ldh, packed, bits, rows, scales, zeros, group, index)
+    if kind == "loss":
+        return lib.gptq_head_loss(*head, loss, lse, zk, ws, wsb, None)
+    if kind == "loss_backward":
+        return lib.gptq_head_loss_backward(*head, lse, zk, dloss, dh, lddh, ws, wsb, None)
+    if kind == "distill":
+        return lib.gptq_head_distill(*head, teacher, top, T, loss, lse, zk, ws, wsb, None)
+    return lib.gptq_head_distill_backward(*head, teacher, top, T, lse, zk, dloss, dh, lddh, ws, wsb,
+                                          None)
+
+
+@pytest.mark.parametrize("kind", ["loss", "loss_backward", "distill", "distill_backward"])
+def test_head_refusals(kind):
+    distill, backward = kind.startswith("distill"), kind.endswith("backward")
+    call = lambda **k: _loss(kind=kind, teacher=k.pop("teacher", FAKE), **k)  # noqa: E731
+    bad = [dict(h=None), dict(packed=None), dict(scales=None), dict(zeros=None), dict(index=None),
+           dict(lse=None), dict(zk=None), dict(m=-1), dict(rows=0), dict(ldh=255), dict(bits=1),
+           dict(lse=FAKE + 2), dict(index=FAKE + 1), dict(group=0)]
+    bad += [dict(dloss=None), dict(dh=None), dict(lddh=255)] if backward else [dict(loss=None)]
+    if distill:
+        bad += [dict(teacher=None), dict(top=0), dict(top=-1), dict(T=0.0), dict(T=-1.0),
+                dict(T=float("inf")), dict(T=float("nan")), dict(T=1e-45)]
+    for b in bad:
+        assert call(**b) == BAD, b
+    unsup = [dict(bits=3), dict(cols=200, ldh=200, lddh=200), dict(group=64), dict(h=FAKE + 2),
+             dict(ldh=260), dict(m=2 ** 23 + 1)] + ([dict(top=257)] if distill else [])
+    for b in unsup:
+        assert call(**b) == UNSUP, b
+    assert call(m=0, h=None, index=None, dh=None) == gq.GPTQ_OK
+    op = gq.OP_HEAD_BACKWARD if backward else gq.OP_HEAD_LOSS
+    need = gq.head_workspace_bytes(op, 4, 500, 256)
+    assert need > 0 and call() == WS and call(ws=FAKE, wsb=need - 1) == WS
+    assert call(ws=FAKE + 64, wsb=need) == BAD
+
+
+def test_workspace_sizes():
+    wb, hb = gq.adapters_workspace_bytes, gq.head_workspace_bytes
+    assert wb(gq.OP_FORWARD_ADAPTERS, 100, 64, 64, 2, 17) == 100 * 32 * 4
+    assert wb(gq.OP_BACKWARD, 100, 64, 128) == 128 * 64 * 2
+    assert wb(gq.OP_BACKWARD, 0, 64, 128, 2, 8) == 0
+    for a in ((gq.OP_BACKWARD, -1, 64, 64, 1, 8), (gq.OP_BACKWARD, 4, 0, 64, 1, 8),
+              (gq.OP_BACKWARD, 4, 64, 64, 1, 129), (gq.OP_BACKWARD, 4, 64, 64, 4097, 8),
+              (gq.OP_BACKWARD, 4, 64, 64, 1, 0), (99, 4, 64, 64, 1, 8)):
+        assert wb(*a) == 0, a
+    assert hb(gq.OP_HEAD_LOSS, 0, 500, 256) == 0 and hb(99, 4, 500, 256) == 0
+    # a gradient's workspace stops growing with the tokens' probabilities (8192
+    # tokens a pass) and with the vocabulary (8192 entries a pass)
+    big = hb(gq.OP_HEAD_BACKWARD, 1 << 20, 32000, 4096)
+    assert big < hb(gq.OP_HEAD_BACKWARD, 8192, 32000, 4096) + (1 << 20) * 8 + 4096
+    assert hb(gq.OP_HEAD_BACKWARD, 64, 1 << 20, 256) <= hb(gq.OP_HEAD_BACKWARD, 64, 1 << 17, 256)
+
+
+def test_python_checks_come_before_the_library():
+    x = torch.zeros((2, 128), dtype=torch.float16)
+    with pytest.raises(ValueError, match="x must be"):
+        gq.dequant_gemm_adapters(x, None, 4, 128, None, None, 128, None, None, None, None)
+    with pytest.raises(ValueError, match="dy must be"):
+        gq.linear_backward(x, None, 4, 128, None, None, 128)
+    with pytest.raises(ValueError, match="h must be"):
+        gq.head_loss(x, None, 4, 128, None, None, 128, None)
+    with pytest.raises(ValueError, match="temperature"):
+        gq.head_distill(x, None, 4, 128, None, None, 128, None, None, temperature=0.0)
