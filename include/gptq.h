@@ -477,9 +477,10 @@ gptq_status gptq_dequant_gemm_adapters(const void* x, int64_t m, int64_t cols, i
 /*
  * gptq_linear_forward_adapters -- gptq_linear_forward (many tokens, fp16 y;
  * the same shapes, alignment and errors) with the tokens' adapters:
- * y = act(x W_hat^T + adapters).  The fp32 sum is rounded to fp16 (a token
- * without an adapter can differ by one fp16 step from gptq_linear_forward
- * without ReLU, whose last addition rounds straight to fp16).
+ * y = act(x W_hat^T + adapters), the layer's part with
+ * gptq_linear_forward's bound, the adapter's with that above, their fp32 sum
+ * rounded to fp16.  The groups' sums may
+ * be added in another order than gptq_linear_forward adds them.
  *   Asynchronous; bitwise deterministic.
  */
 gptq_status gptq_linear_forward_adapters(const void* x, int64_t m, int64_t cols, int64_t ldx,

@@ -162,8 +162,11 @@ hipError_t launch_dequant_gemv_adapters(const _Float16* x, int64_t ldx, int64_t 
 hipError_t launch_linear_forward_adapters(int bits, const _Float16* x, int64_t ldx, int64_t m,
                                           const uint32_t* packed, int64_t rows, int64_t cols,
                                           const float* scales, const float* zeros, int groupsize,
-                                          bool relu, const AdapterTile& ad, _Float16* y,
-                                          int64_t ldy, hipStream_t s);
+                                          bool relu, const AdapterTile& ad, float* sums,
+                                          _Float16* y, int64_t ldy, hipStream_t s);
+// splits of the input columns when the tiles leave CUs idle (1: none); their
+// fp32 sums, splits x m x rows, go to the workspace
+int linear_splits(int bits, int64_t m, int64_t rows, int64_t cols, int groupsize);
 // the transposed weights and the products with them
 constexpr int kKPad = 64;  // K of the fp16 product, padded with zeros
 hipError_t launch_dequant_transposed(const uint32_t* packed, int bits, int64_t rows, int64_t cols,
@@ -180,17 +183,6 @@ hipError_t launch_gemm_nt_acc(const _Float16* A, int64_t lda, int64_t m, const _
                               int64_t ldb, int64_t n, int64_t K, bool first, float* C32,
                               const float* scale, _Float16* C16, int64_t ldc, hipStream_t s);
 // the vocabulary losses
-int64_t head_tiles(int bits, int64_t rows);
-// part[tile][t] = (max, sum exp(z - max)) over the tile's outputs, z = (x W_hat^T) inv_t
-hipError_t launch_head_partials(int bits, const _Float16* x, int64_t ldx, int64_t m,
-                                const uint32_t* packed, int64_t rows, int64_t cols,
-                                const float* scales, const float* zeros, int groupsize,
-                                float inv_t, float2* part, hipStream_t s);
-// P[t][r] = exp(z - lse[t]) in fp16, 0 where lse[t] is +inf and for rows <= r < ldp
-hipError_t launch_head_probs(int bits, const _Float16* x, int64_t ldx, int64_t m,
-                             const uint32_t* packed, int64_t rows, int64_t cols,
-                             const float* scales, const float* zeros, int groupsize, float inv_t,
-                             const float* lse, _Float16* P, int64_t ldp, hipStream_t s);
 // what is learnt: K entries per token, logits (their softmax) or one label
 struct HeadTargets {
   const int* index;     // m x top
@@ -199,11 +191,22 @@ struct HeadTargets {
   float inv_t;
 };
 constexpr int kMaxTop = 256;
-hipError_t launch_head_finish(int bits, const _Float16* h, int64_t ldh, int64_t m,
-                              const uint32_t* packed, int64_t rows, int64_t cols,
-                              const float* scales, const float* zeros, int groupsize,
-                              const HeadTargets& tg, const float2* part, int64_t tiles,
-                              float* loss, float* lse, float* zk, hipStream_t s);
+int64_t head_tiles(int bits, int64_t m, int64_t rows);
+// part[tile][t] = (max, sum exp(z - max)) over the tile's outputs, z = (x
+// W_hat^T) inv_t, and zk[t][k] = z of the named outputs inside [0, rows)
+hipError_t launch_head_partials(int bits, const _Float16* x, int64_t ldx, int64_t m,
+                                const uint32_t* packed, int64_t rows, int64_t cols,
+                                const float* scales, const float* zeros, int groupsize,
+                                const HeadTargets& tg, float2* part, float* zk, hipStream_t s);
+// P[t][r] = exp(z - lse[t]) in fp16, 0 where lse[t] is +inf and for rows <= r < ldp
+hipError_t launch_head_probs(int bits, const _Float16* x, int64_t ldx, int64_t m,
+                             const uint32_t* packed, int64_t rows, int64_t cols,
+                             const float* scales, const float* zeros, int groupsize, float inv_t,
+                             const float* lse, _Float16* P, int64_t ldp, hipStream_t s);
+// lse and the loss from the tiles' partials and the named logits (zk: 0 where
+// an entry takes no part)
+hipError_t launch_head_finish(int64_t m, int64_t rows, const HeadTargets& tg, const float2* part,
+                              int64_t tiles, float* loss, float* lse, float* zk, hipStream_t s);
 // lse_eff[t] = lse[t] or +inf, gscale[t] = dloss[t] inv_t or 0 (no entries)
 hipError_t launch_head_rows(const HeadTargets& tg, int64_t m, int64_t rows, const float* lse,
                             const float* dloss, float* lse_eff, float* gscale, hipStream_t s);

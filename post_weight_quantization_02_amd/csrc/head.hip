@@ -1,8 +1,7 @@
 // Losses through a stored vocabulary projection, z = W_hat h / T, with the
-// logits never kept: the statistics of the softmax come from the product's
-// own tiles (launch_head_partials), the few logits that the targets name are
-// formed here from the packed rows, and the gradient takes the softmax one
-// piece of the vocabulary at a time.
+// logits never kept: the statistics of the softmax and the few logits that the
+// targets name come from the product's own tiles (launch_head_partials), and
+// the gradient takes the softmax one piece of the vocabulary at a time.
 //
 //   labels        loss = lse(z) - z_y
 //   distillation  p = softmax(teacher / T) over the K entries given,
@@ -59,19 +58,15 @@ __device__ inline float log_p(const HeadTargets& tg, int64_t t, int k, float tls
   return tg.logits == nullptr ? 0.f : tg.logits[t * tg.top + k] * tg.inv_t - tlse;
 }
 
-// One token per workgroup: lse from the tiles' partials, the named logits
-// (one wave each, exact products summed in fp32) and the loss.
-template <int BITS>
-__global__ __launch_bounds__(256) void head_finish_kernel(
-    const _Float16* __restrict__ h, int64_t ldh, int64_t m, const uint32_t* __restrict__ packed,
-    int64_t nw, int64_t rows, const float* __restrict__ scales, const float* __restrict__ zeros,
-    int64_t ngroups, int groupsize, HeadTargets tg, const float2* __restrict__ part, int64_t tiles,
-    float* __restrict__ loss, float* __restrict__ lse_out, float* __restrict__ zk) {
-  constexpr int K = 32 / BITS;
-  constexpr uint32_t MASK = (1u << BITS) - 1u;
-  __shared__ float sums[4];
-  const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+// One token per wave.
+__global__ __launch_bounds__(256) void head_finish_kernel(int64_t m, int64_t rows, HeadTargets tg,
+                                                          const float2* __restrict__ part,
+                                                          int64_t tiles, float* __restrict__ loss,
+                                                          float* __restrict__ lse_out,
+                                                          float* __restrict__ zk) {
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (t >= m) return;
   float top = -INFINITY;
   for (int64_t i = lane; i < tiles; i += 64) top = fmaxf(top, part[i * m + t].x);
   top = wave_max(top);
@@ -84,35 +79,17 @@ __global__ __launch_bounds__(256) void head_finish_kernel(
   const float lse = base + __logf(wave_sum(sum));
   bool any;
   const float tlse = teacher_lse(tg, t, rows, &any);
-
-  const _Float16* x = h + t * ldh;
-  float part_loss = 0.f;
-  for (int k = wave; k < tg.top; k += waves) {
-    float z = 0.f;
-    const bool in = takes_part(tg, t, k, rows);
-    if (in) {  // the same for the whole wave
-      const int64_t r = tg.index[t * tg.top + k];
-      for (int64_t w = lane; w < nw; w += 64) {
-        const uint32_t q = packed[r * nw + w];
-        const int64_t g = w * K / groupsize;
-        const float zero = zeros[r * ngroups + g];
-        float d = 0.f;
-#pragma unroll
-        for (int j = 0; j < K; ++j)
-          d = __builtin_fmaf((float)x[w * K + j], (float)((q >> (BITS * j)) & MASK) - zero, d);
-        z = __builtin_fmaf(scales[r * ngroups + g], d, z);
-      }
-      z = wave_sum(z) * tg.inv_t;
+  float l = 0.f;
+  for (int k = lane; k < tg.top; k += 64) {
+    if (takes_part(tg, t, k, rows)) {
       const float lp = log_p(tg, t, k, tlse);
-      part_loss += __expf(lp) * (lp - z + lse);
+      l += __expf(lp) * (lp - zk[t * tg.top + k] + lse);
+    } else {
+      zk[t * tg.top + k] = 0.f;
     }
-    if (lane == 0) zk[t * tg.top + k] = z;
   }
-  if (lane == 0) sums[wave] = part_loss;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float l = 0.f;
-    for (int w = 0; w < waves; ++w) l += sums[w];
+  l = wave_sum(l);
+  if (lane == 0) {
     loss[t] = any ? l : 0.f;
     lse_out[t] = lse;
   }
@@ -161,19 +138,10 @@ __global__ __launch_bounds__(64) void head_scatter_kernel(HeadTargets tg, int64_
 
 }  // namespace
 
-hipError_t launch_head_finish(int bits, const _Float16* h, int64_t ldh, int64_t m,
-                              const uint32_t* packed, int64_t rows, int64_t cols,
-                              const float* scales, const float* zeros, int groupsize,
-                              const HeadTargets& tg, const float2* part, int64_t tiles,
-                              float* loss, float* lse, float* zk, hipStream_t s) {
-  const dim3 block(64 * (tg.top < 4 ? tg.top : 4));
-  const int64_t nw = packed_words(cols, bits), ng = ceil_div(cols, groupsize);
-  if (bits == 4)
-    hipLaunchKernelGGL(head_finish_kernel<4>, dim3((unsigned)m), block, 0, s, h, ldh, m, packed, nw,
-                       rows, scales, zeros, ng, groupsize, tg, part, tiles, loss, lse, zk);
-  else
-    hipLaunchKernelGGL(head_finish_kernel<8>, dim3((unsigned)m), block, 0, s, h, ldh, m, packed, nw,
-                       rows, scales, zeros, ng, groupsize, tg, part, tiles, loss, lse, zk);
+hipError_t launch_head_finish(int64_t m, int64_t rows, const HeadTargets& tg, const float2* part,
+                              int64_t tiles, float* loss, float* lse, float* zk, hipStream_t s) {
+  hipLaunchKernelGGL(head_finish_kernel, dim3((unsigned)ceil_div(m, 4)), dim3(256), 0, s, m, rows,
+                     tg, part, tiles, loss, lse, zk);
   return hipGetLastError();
 }
 

@@ -40,16 +40,14 @@
 namespace gptq {
 namespace {
 
-constexpr int TM = 128;    // tokens per workgroup
 constexpr int KG = 128;    // input columns per stage
 constexpr int NSTAGE = 3;
-constexpr int X_BYTES = TM * KG * 2;  // 32 KB
-constexpr int NWAVE = 8;
-constexpr int AT = TM / 16;           // a-tiles per wave (each wave owns all 128 tokens)
 constexpr int kXcds = 8;
 constexpr int kGroupM = 4;  // token tiles per XCD-local group
 
-// What depends on the code width.  `piece` is the XOR swizzle of the 16-byte
+// What depends on the code width: a wave's outputs (WTN), the packed bytes of
+// one output row per stage (RB), and the 16-byte pieces per lane per stage
+// (LP).  `piece` is the XOR swizzle of the 16-byte
 // pieces of a stage's packed row: the 16-byte reads of 16 consecutive rows at
 // one logical piece hit distinct bank groups, for 8- and for 16-lane LDS
 // service groups.
@@ -57,34 +55,41 @@ template <int BITS>
 struct Geo;
 template <>
 struct Geo<4> {
-  static constexpr int TN = 256;  // outputs per workgroup
-  static constexpr int RB = 64;   // packed bytes of one output row per stage
-  static constexpr int LP = 1;    // 16-byte pieces per lane per stage
+  static constexpr int WTN = 32;
+  static constexpr int RB = 64;
+  static constexpr int LP = 1;
   __device__ static int piece(int row, int p) { return p ^ (((row >> 1) ^ (row >> 2)) & 3); }
 };
 template <>
 struct Geo<8> {
-  static constexpr int TN = 128;
+  static constexpr int WTN = 16;
   static constexpr int RB = 128;
   static constexpr int LP = 2;
   __device__ static int piece(int row, int p) { return p ^ ((row ^ (row >> 3)) & 7); }
 };
 
-template <int BITS>
+// A workgroup of W waves owns 16 A tokens x W * WTN outputs (every wave all of
+// the tokens).  <8, 8>, 128 tokens x 256 (4 bits) or 128 (8 bits) outputs, is
+// the shape for many tokens.
+template <int BITS_, int A, int W>
 struct Lay {
-  static constexpr int TN = Geo<BITS>::TN, RB = Geo<BITS>::RB, LP = Geo<BITS>::LP;
+  static constexpr int BITS = BITS_;
+  static constexpr int AT = A, NWAVE = W, TM = 16 * A;
+  static constexpr int RB = Geo<BITS>::RB, LP = Geo<BITS>::LP;
+  static constexpr int WTN = Geo<BITS>::WTN, TN = W * WTN;
+  static constexpr int X_BYTES = TM * KG * 2;  // 32 KB at 128 tokens
   static constexpr int PPR = RB / 16;          // pieces per packed row
-  static constexpr int B_BYTES = TN * RB;      // 16 KB
+  static constexpr int B_BYTES = TN * RB;      // 16 KB with eight waves
   static constexpr int S_BYTES = TN * 4;       // scales (zeros follow)
   static constexpr int STAGE = X_BYTES + B_BYTES + 2 * S_BYTES;
-  static constexpr int WTN = TN / NWAVE;       // outputs per wave
   static constexpr int BT = WTN / 16;          // b-tiles per wave
   static constexpr int BROWS = 1024 / RB;      // packed rows per 1 KB wave load
   static constexpr int XU = X_BYTES / 1024 / NWAVE;  // x loads per wave per stage
   static constexpr int WU = B_BYTES / 1024 / NWAVE;  // word loads per wave per stage
   static constexpr int SZL = 2 * S_BYTES / 256;      // 256-byte scale/zero loads per stage
   static constexpr int LOADS_PER_STAGE = XU + WU + 1;
-  static_assert(B_BYTES == 16384 && XU == 4 && WU == 2 && SZL <= NWAVE, "stage layout");
+  static_assert(WU == 2 && XU >= 1 && XU * 1024 * NWAVE == X_BYTES && SZL >= 2 && SZL <= NWAVE,
+                "stage layout");
 };
 
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
@@ -151,27 +156,27 @@ __device__ inline half8 codes_minus_zero8(uint32_t w0, uint32_t w1, half2_t off)
 // clamped rows, swizzled pieces.  They fit 32 bits (at most 256 rows of at
 // most 2^22 bytes, plus the column offset), so the loads use a scalar base and
 // one VGPR each.
-template <int BITS>
+template <class L>
 struct DmaOffsets {
-  uint32_t x[Lay<BITS>::XU];  // x: wave loads of 4 rows x 256 bytes
-  uint32_t w[Lay<BITS>::WU];  // packed words: wave loads of 1 KB of packed rows
-  uint32_t sz;                // the scales or zeros of 64 outputs
+  uint32_t x[L::XU];  // x: wave loads of 4 rows x 256 bytes
+  uint32_t w[L::WU];  // packed words: wave loads of 1 KB of packed rows
+  uint32_t sz;        // the scales or zeros of 64 outputs
 };
 
 // Load q = wave % SZL of a stage's scale/zero loads: the scales (q < SZL / 2)
 // or zeros of outputs 64 (q % (SZL / 2)) + 0..63.  With SZL < NWAVE (8 bits)
 // waves q and q + SZL issue the same load, so every wave issues one.
-template <int BITS>
+template <class L>
 __device__ inline int sz_load(int wave) {
-  return wave % Lay<BITS>::SZL;
+  return wave % L::SZL;
 }
 
-template <int BITS>
-__device__ inline DmaOffsets<BITS> dma_offsets(int64_t ldx, int64_t t0, int64_t m, int64_t nw,
-                                               int64_t ngroups, int64_t n0, int64_t rows,
-                                               int wave, int lane) {
-  using L = Lay<BITS>;
-  DmaOffsets<BITS> d;
+template <class L>
+__device__ inline DmaOffsets<L> dma_offsets(int64_t ldx, int64_t t0, int64_t m, int64_t nw,
+                                            int64_t ngroups, int64_t n0, int64_t rows, int wave,
+                                            int lane) {
+  constexpr int BITS = L::BITS, NWAVE = L::NWAVE;
+  DmaOffsets<L> d;
 #pragma unroll
   for (int u = 0; u < L::XU; ++u) {
     const int row = 4 * (wave + NWAVE * u) + (lane >> 4);
@@ -184,17 +189,17 @@ __device__ inline DmaOffsets<BITS> dma_offsets(int64_t ldx, int64_t t0, int64_t 
     const int64_t r = min(n0 + row, rows - 1) - n0;
     d.w[u] = (uint32_t)(r * nw * 4 + 16 * Geo<BITS>::piece(row, lane % L::PPR));
   }
-  const int q = sz_load<BITS>(wave);
+  const int q = sz_load<L>(wave);
   const int64_t r = min(n0 + 64 * (q % (L::SZL / 2)) + lane, rows - 1) - n0;
   d.sz = (uint32_t)(r * ngroups * 4);
   return d;
 }
 
-// Issue one stage's direct loads (input columns c0..c0+127) into `st`.
-template <int BITS>
+// Issue the direct loads of chunk k (input columns 128 k..128 k + 127) into `st`.
+template <class L>
 __device__ inline void issue_stage(const char* xb, const char* wbase, const char* szb,
-                                   const DmaOffsets<BITS>& d, int k, int grp, char* st, int wave) {
-  using L = Lay<BITS>;
+                                   const DmaOffsets<L>& d, int k, int grp, char* st, int wave) {
+  constexpr int BITS = L::BITS, NWAVE = L::NWAVE, X_BYTES = L::X_BYTES;
   const uint32_t c0 = (uint32_t)k * KG;
   // the column offset goes into the 32-bit lane offset (at most 2^21 more),
   // which keeps each address a scalar base plus one VGPR inside the loop
@@ -210,18 +215,26 @@ __device__ inline void issue_stage(const char* xb, const char* wbase, const char
                                      0);
   __builtin_amdgcn_global_load_lds(
       (const void*)(szb + (d.sz + cs)),
-      (lds_void*)(st + X_BYTES + L::B_BYTES + 256 * sz_load<BITS>(wave)), 4, 0, 0);
+      (lds_void*)(st + X_BYTES + L::B_BYTES + 256 * sz_load<L>(wave)), 4, 0, 0);
 }
 
-// Position of a stage inside its scale group (groups are gk stages long);
-// kept as running counters so the loop does no division.
+// The chunk of a stage, and its place inside its scale group (groups are gk
+// chunks long); running counters, so the loop does no division.  A
+// workgroup's chunks are [begin, end), whole groups, taken from the first
+// chunk of some group on and around.
 struct GroupCursor {
-  int in = 0;   // stage index inside the group
-  int grp = 0;  // group index
-  __device__ void advance(int gk) {
+  int chunk, in, grp;
+  __device__ GroupCursor(int group, int gk) : chunk(group * gk), in(0), grp(group) {}
+  __device__ void advance(int gk, int begin, int end, int first) {
+    ++chunk;
     if (++in == gk) {
       in = 0;
       ++grp;
+    }
+    if (chunk == end) {
+      chunk = begin;
+      in = 0;
+      grp = first;
     }
   }
 };
@@ -238,7 +251,7 @@ struct LaneOffsets {
 };
 
 // acc += scale * partial for every output of the lane (the group's last stage)
-template <int BT>
+template <int AT, int BT>
 __device__ inline void fold_group(f32x4 (&acc)[AT][BT], const f32x4 (&part)[AT][BT],
                                   const float (&fsc)[BT]) {
 #pragma unroll
@@ -255,16 +268,14 @@ __device__ inline void fold_group(f32x4 (&acc)[AT][BT], const f32x4 (&part)[AT][
 // The stages are three distinct LDS arrays named at compile time, so the
 // compiler can tell that reading `cur` does not touch the direct loads still
 // landing in the other two and adds no wait for them.
-template <int BITS>
+template <class L>
 __device__ inline void stage_step(int k, int nk, const char* cur, char* nxt, const char* xb,
-                                  const char* wbase, const char* szb,
-                                  const DmaOffsets<BITS>& dm, int gk, GroupCursor& use,
-                                  GroupCursor& iss, int wave, const LaneOffsets<BITS>& lo,
-                                  f32x4 (&acc)[AT][Lay<BITS>::BT],
-                                  f32x4 (&part)[AT][Lay<BITS>::BT], bool& fold,
-                                  float (&fsc)[Lay<BITS>::BT]) {
-  using L = Lay<BITS>;
-  constexpr int BT = L::BT;
+                                  const char* wbase, const char* szb, const DmaOffsets<L>& dm,
+                                  int gk, int kb, int ke, int gb, GroupCursor& use, GroupCursor& iss,
+                                  int wave, const LaneOffsets<L::BITS>& lo,
+                                  f32x4 (&acc)[L::AT][L::BT], f32x4 (&part)[L::AT][L::BT],
+                                  bool& fold, float (&fsc)[L::BT]) {
+  constexpr int BITS = L::BITS, AT = L::AT, BT = L::BT, X_BYTES = L::X_BYTES;
   // stage k has landed for this wave; stage k + 1 may still be in flight
   if (k + 1 < nk) wait_vm<L::LOADS_PER_STAGE>();
   else wait_vm<0>();
@@ -292,20 +303,20 @@ __device__ inline void stage_step(int k, int nk, const char* cur, char* nxt, con
     for (int h = 0; h < L::LP; ++h)
       wb[b][h] = *reinterpret_cast<const uint4*>(sb + lo.w[h] + 16 * L::RB * b);
   if (k + 2 < nk) {
-    issue_stage<BITS>(xb, wbase, szb, dm, k + 2, iss.grp, nxt, wave);
-    iss.advance(gk);
+    issue_stage<L>(xb, wbase, szb, dm, iss.chunk, iss.grp, nxt, wave);
+    iss.advance(gk, kb, ke, gb);
   }
   // The previous group's partial sums enter the running sums here, after the
   // barrier, where these FMAs fill the wait for this stage's first LDS reads
   // instead of delaying the barrier.
   if (fold) {
-    fold_group<BT>(acc, part, fsc);
+    fold_group<AT, BT>(acc, part, fsc);
     fold = false;
   }
 
   const bool gstart = use.in == 0;
-  const bool gend = use.in == gk - 1 || k + 1 == nk;
-  use.advance(gk);
+  const bool gend = use.in == gk - 1 || use.chunk + 1 == ke;
+  use.advance(gk, kb, ke, gb);
   const half2_t mul = {(_Float16)1.0f, (_Float16)0.0625f};
   const uint32_t magic = 0x64006400u;
 #pragma unroll
@@ -352,26 +363,32 @@ __device__ inline void stage_step(int k, int nk, const char* cur, char* nxt, con
 // What becomes of a tile's sums:
 //   kStore     fp16 outputs, the layer's own product
 //   kAdapters  the adapters' part added first (adapters_dev.h)
+//   kSplit     fp32 sums of one split of the input columns
 //   kPartials  z = sum * inv_t: per token the tile's max and sum exp(z - max),
 //              the pieces of the softmax statistics of a vocabulary whose
-//              logits are not kept
+//              logits are not kept, and the logits that the targets name
 //   kProbs     exp(z - lse) in fp16, the softmax of one piece of it
-enum TailMode { kStore = 0, kAdapters = 1, kPartials = 2, kProbs = 3 };
+enum TailMode { kStore = 0, kAdapters = 1, kSplit = 2, kPartials = 3, kProbs = 4 };
 struct Tail {
   AdapterTile ad;
+  float* sums;       // splits x m x rows
   float inv_t;
   float2* part;      // output tiles x m
   const float* lse;  // m
+  const int* index;  // m x top
+  int top;
+  float* zk;         // m x top
 };
 
-// (max, sum exp(z - max)) of the tile's outputs for each of its 128 tokens:
-// over the wave's outputs in registers and 16-lane shuffles, over the waves
-// through LDS.  Outputs past the matrix count as -inf.
-template <int BT>
-__device__ inline void tile_partials(const f32x4 (&acc)[AT][BT], const Tail& tail, float2* red,
-                                     int64_t t0, int64_t m, int64_t tn, int64_t nw, int64_t rows) {
+// (max, sum exp(z - max)) of the tile's outputs for each of its tokens: over
+// the wave's outputs in registers and 16-lane shuffles, over the waves through
+// LDS.  Outputs past the matrix count as -inf.
+template <class L>
+__device__ inline void tile_partials(const f32x4 (&acc)[L::AT][L::BT], const Tail& tail,
+                                     float2* red, int64_t t0, int64_t m, int64_t tn, int64_t nw,
+                                     int64_t rows) {
+  constexpr int AT = L::AT, BT = L::BT, TM = L::TM, NWAVE = L::NWAVE;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, kg = lane >> 4;
-  __syncthreads();  // the stages are free
 #pragma unroll
   for (int a = 0; a < AT; ++a)
 #pragma unroll
@@ -408,36 +425,85 @@ __device__ inline void tile_partials(const f32x4 (&acc)[AT][BT], const Tail& tai
   }
 }
 
-template <int BITS, bool RELU, int TAIL>
-__global__ __launch_bounds__(512, 1) void linear_kernel(
+// zk[t][k] = z[t][index[t][k]] for the named outputs inside the tile: 16
+// tokens' sums at a time go through LDS, and every thread looks its share of
+// the 16 x top entries up.
+template <class L>
+__device__ inline void tile_targets(const f32x4 (&acc)[L::AT][L::BT], const Tail& tail, float* zs,
+                                    int64_t t0, int64_t m, int64_t n0, int64_t rows) {
+  constexpr int PITCH = L::TN + 4;  // rows 4 banks apart
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, kg = lane >> 4;
+  const int64_t end = min(n0 + L::TN, rows);
+#pragma unroll
+  for (int a = 0; a < L::AT; ++a) {
+    if (t0 + 16 * a >= m) break;
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < L::BT; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        zs[(4 * kg + i) * PITCH + L::WTN * wave + 16 * b + li] = acc[a][b][i];
+    __syncthreads();
+    const int n = (int)min((int64_t)16, m - t0 - 16 * a) * tail.top;
+    const int64_t e0 = (t0 + 16 * a) * tail.top;
+    for (int e = tid; e < n; e += 64 * L::NWAVE) {
+      const int64_t v = tail.index[e0 + e];
+      if (v >= n0 && v < end) tail.zk[e0 + e] = zs[(e / tail.top) * PITCH + (v - n0)] * tail.inv_t;
+    }
+  }
+}
+
+// The grid of one product: which tiles an XCD works on, and in which order.
+// Workgroup b runs on XCD b % 8.  The XCDs form an xm x (8 / xm) grid over the
+// token and output tiles; an XCD walks its token tiles in groups of gm, and
+// within a group output tile by output tile, so the ~32 workgroups it runs
+// at once share 4 x tiles and 8 weight tiles in its L2 (32 KB and 16 KB per
+// stage: the split that minimises its misses).  With fewer than 32 token
+// tiles xm falls below 8 so that an XCD still has 4 of them and the weights
+// are read by 8 / xm fewer XCDs.
+struct TileGrid {
+  int64_t ntm, ntn;
+  int xm, gm;
+};
+
+// The weights of one chunk are 64 (128) bytes of every packed row: rows whose
+// pitch is a multiple of 2 KB put them on an eighth of the memory channels,
+// and workgroups that run in step read them all at once.  With `rotate` each
+// XCD starts at another chunk (an eighth of the row further) and goes around,
+// which uses all channels: 2.2x (8 bits) to 4x on the short vocabulary cases.
+// The layer's own product (kStore) keeps its order of addition.
+template <int BITS, bool RELU, int TAIL, int A, int W>
+__global__ __launch_bounds__(64 * W, 1) void linear_kernel(
     const _Float16* __restrict__ x, int64_t ldx, int64_t m, const uint32_t* __restrict__ packed,
     int64_t nw, int64_t rows, int64_t cols, const float* __restrict__ scales,
-    const float* __restrict__ zeros, int64_t ngroups, int gk, int64_t ntn, int64_t ntm,
+    const float* __restrict__ zeros, int64_t ngroups, int gk, TileGrid grid,
     _Float16* __restrict__ y, int64_t ldy, Tail tail) {
-  using L = Lay<BITS>;
-  constexpr int BT = L::BT;
+  using L = Lay<BITS, A, W>;
+  constexpr int AT = L::AT, BT = L::BT;
   __shared__ __attribute__((aligned(1024))) char st0[L::STAGE];
   __shared__ __attribute__((aligned(1024))) char st1[L::STAGE];
   __shared__ __attribute__((aligned(1024))) char st2[L::STAGE];
 
-  // XCD-aware tile order.  Workgroup b runs on XCD b % 8, which takes token
-  // tiles xcd, xcd + 8, ...; its local index walks them in groups of kGroupM
-  // token tiles, and within a group output tile by output tile, so the ~32
-  // workgroups an XCD runs at once share 4 x tiles and 8 weight tiles in its
-  // L2 (32 KB and 16 KB per stage: the split that minimises its misses).
   const int64_t bid = blockIdx.x;
-  const int64_t xcd = bid % kXcds, local = bid / kXcds;
-  const int64_t grp = local / (kGroupM * ntn), idx = local % (kGroupM * ntn);
-  const int64_t tm = (grp * kGroupM + idx % kGroupM) * kXcds + xcd;
-  const int64_t tn = idx / kGroupM;
-  if (tm >= ntm) return;
-  const int64_t t0 = tm * TM, n0 = tn * L::TN;
+  const int xcd = (int)(bid % kXcds);
+  const int64_t local = bid / kXcds;
+  const int xi = xcd % grid.xm, xj = xcd / grid.xm, xn = kXcds / grid.xm;
+  const int64_t ntj = (grid.ntn + xn - 1) / xn;
+  const int64_t grp = local / (grid.gm * ntj), idx = local % (grid.gm * ntj);
+  const int64_t tm = (grp * grid.gm + idx % grid.gm) * grid.xm + xi;
+  const int64_t tn = (idx / grid.gm) * xn + xj;
+  if (tm >= grid.ntm || tn >= grid.ntn) return;
+  const int64_t t0 = tm * L::TM, n0 = tn * L::TN;
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // uniform: scalar bases
   const int li = lane & 15, kg = lane >> 4;
-  const int nk = (int)(cols / KG);
+  // this split's groups [gb, ge) and chunks [kb, ke), and the group it starts at
+  const int gb = TAIL == kSplit ? (int)(ngroups * blockIdx.y / gridDim.y) : 0;
+  const int ge = TAIL == kSplit ? (int)(ngroups * (blockIdx.y + 1) / gridDim.y) : (int)ngroups;
+  const int kb = gb * gk, ke = min(ge * gk, (int)(cols / KG)), nk = ke - kb;
+  const int start = TAIL == kStore ? gb : gb + (ge - gb) * xcd / kXcds;
   LaneOffsets<BITS> lo;
 #pragma unroll
   for (int s = 0; s < 4; ++s) lo.x[s] = 256 * li + 16 * x_piece(li, 4 * kg + s);
@@ -455,38 +521,41 @@ __global__ __launch_bounds__(512, 1) void linear_kernel(
 #pragma unroll
     for (int b = 0; b < BT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const DmaOffsets<BITS> dm = dma_offsets<BITS>(ldx, t0, m, nw, ngroups, n0, rows, wave, lane);
+  const DmaOffsets<L> dm = dma_offsets<L>(ldx, t0, m, nw, ngroups, n0, rows, wave, lane);
   const char* xb = reinterpret_cast<const char*>(x + t0 * ldx);
   const char* wbase = reinterpret_cast<const char*>(packed + n0 * nw);
   const char* szb = reinterpret_cast<const char*>(
-      (sz_load<BITS>(wave) < L::SZL / 2 ? scales : zeros) + n0 * ngroups);
+      (sz_load<L>(wave) < L::SZL / 2 ? scales : zeros) + n0 * ngroups);
 
-  GroupCursor use, iss;
-  issue_stage<BITS>(xb, wbase, szb, dm, 0, iss.grp, st0, wave);
-  iss.advance(gk);
+  GroupCursor use(start, gk), iss(start, gk);
+  issue_stage<L>(xb, wbase, szb, dm, iss.chunk, iss.grp, st0, wave);
+  iss.advance(gk, kb, ke, gb);
   if (nk > 1) {
-    issue_stage<BITS>(xb, wbase, szb, dm, 1, iss.grp, st1, wave);
-    iss.advance(gk);
+    issue_stage<L>(xb, wbase, szb, dm, iss.chunk, iss.grp, st1, wave);
+    iss.advance(gk, kb, ke, gb);
   }
   bool fold = false;
   float fsc[BT];
   for (int k = 0; k < nk; k += NSTAGE) {
-    stage_step<BITS>(k, nk, st0, st2, xb, wbase, szb, dm, gk, use, iss, wave, lo, acc, part, fold,
-                     fsc);
+    stage_step<L>(k, nk, st0, st2, xb, wbase, szb, dm, gk, kb, ke, gb, use, iss, wave, lo, acc,
+                  part, fold, fsc);
     if (k + 1 < nk)
-      stage_step<BITS>(k + 1, nk, st1, st0, xb, wbase, szb, dm, gk, use, iss, wave, lo, acc, part,
-                       fold, fsc);
+      stage_step<L>(k + 1, nk, st1, st0, xb, wbase, szb, dm, gk, kb, ke, gb, use, iss, wave, lo,
+                    acc, part, fold, fsc);
     if (k + 2 < nk)
-      stage_step<BITS>(k + 2, nk, st2, st1, xb, wbase, szb, dm, gk, use, iss, wave, lo, acc, part,
-                       fold, fsc);
+      stage_step<L>(k + 2, nk, st2, st1, xb, wbase, szb, dm, gk, kb, ke, gb, use, iss, wave, lo,
+                    acc, part, fold, fsc);
   }
-  fold_group<BT>(acc, part, fsc);  // the last stage always ends a group
+  fold_group<AT, BT>(acc, part, fsc);  // the last stage always ends a group
 
   if constexpr (TAIL == kAdapters)
     add_adapters<AT, BT>(acc, tail.ad, t0, m, n0 + L::WTN * wave, rows);
   if constexpr (TAIL == kPartials) {
-    tile_partials<BT>(acc, tail, reinterpret_cast<float2*>(st0), t0, m, tn, n0 + L::WTN * wave,
-                      rows);
+    static_assert(L::TM * L::NWAVE * 8 <= L::STAGE && 16 * (L::TN + 4) * 4 <= L::STAGE, "LDS");
+    __syncthreads();  // the stages are free
+    tile_partials<L>(acc, tail, reinterpret_cast<float2*>(st0), t0, m, tn, n0 + L::WTN * wave,
+                     rows);
+    tile_targets<L>(acc, tail, reinterpret_cast<float*>(st1), t0, m, n0, rows);
     return;
   }
 
@@ -513,44 +582,103 @@ __global__ __launch_bounds__(512, 1) void linear_kernel(
         const int64_t r = n0 + L::WTN * wave + 16 * b + li;
         if (r >= rows) continue;
         float v = acc[a][b][i];
+        if constexpr (TAIL == kSplit) {
+          tail.sums[((int64_t)blockIdx.y * m + t) * rows + r] = v;
+          continue;
+        }
         if (RELU) v = v > 0.f ? v : 0.f;
         y[t * ldy + r] = (_Float16)v;
       }
     }
 }
 
-int64_t linear_blocks(int bits, int64_t m, int64_t rows) {
-  const int tn = bits == 4 ? Geo<4>::TN : Geo<8>::TN;
-  // every XCD gets the same whole number of kGroupM-token-tile groups
-  return kXcds * round_up(ceil_div(ceil_div(m, TM), kXcds), kGroupM) * ceil_div(rows, tn);
+// The splits of a product added in order, the adapters' part, ReLU, fp16.
+template <bool RELU>
+__global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restrict__ sums,
+                                                            int splits, int64_t m, int64_t rows,
+                                                            AdapterTile ad, _Float16* __restrict__ y,
+                                                            int64_t ldy) {
+  const int64_t t = blockIdx.x, r = (int64_t)blockIdx.y * 256 + threadIdx.x;
+  if (r >= rows) return;
+  float v = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < splits; ++k) v += sums[(k * m + t) * rows + r];
+  const int a = ad.index[t];
+  if (a >= 0 && a < ad.count) {
+    const _Float16* up = ad.up + a * ad.stride + r * ad.ns;
+    float low = 0.f;
+#pragma unroll 4
+    for (int j = 0; j < ad.rank; ++j)
+      low = __builtin_fmaf(ad.v[t * ad.ldv + j], (float)up[j * ad.js], low);
+    v += low;
+  }
+  if (RELU) v = v > 0.f ? v : 0.f;
+  y[t * ldy + r] = (_Float16)v;
 }
 
-template <int BITS, bool RELU, int TAIL>
-hipError_t launch_tail(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed,
-                       int64_t rows, int64_t cols, const float* scales, const float* zeros,
-                       int groupsize, const Tail& tail, _Float16* y, int64_t ldy, hipStream_t s) {
-  const int g = groupsize >= cols ? (int)cols : groupsize;
-  const int64_t ngroups = ceil_div(cols, g);
-  const int gk = (int)ceil_div(g, KG);  // stages per group (a short last group ends at cols)
-  const int64_t nw = cols * BITS / 32;
-  const int64_t ntm = ceil_div(m, TM), ntn = ceil_div(rows, Geo<BITS>::TN);
-  const int64_t blocks = linear_blocks(BITS, m, rows);
-  hipLaunchKernelGGL((linear_kernel<BITS, RELU, TAIL>), dim3((unsigned)blocks), dim3(64 * NWAVE), 0,
-                     s, x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups, gk, ntn, ntm, y,
-                     ldy, tail);
+template <class L>
+TileGrid tile_grid(int64_t m, int64_t rows, bool store) {
+  TileGrid g;
+  g.ntm = ceil_div(m, L::TM);
+  g.ntn = ceil_div(rows, L::TN);
+  g.xm = kXcds;
+  if (!store)
+    while (g.xm > 1 && g.ntm < g.xm * kGroupM) g.xm /= 2;
+  const int64_t mine = ceil_div(g.ntm, g.xm);
+  g.gm = store || mine > kGroupM ? kGroupM : (int)mine;
+  return g;
+}
+
+int64_t grid_blocks(const TileGrid& g) {
+  // every XCD gets the same whole number of gm-token-tile groups
+  return kXcds * round_up(ceil_div(g.ntm, g.xm), g.gm) * ceil_div(g.ntn, kXcds / g.xm);
+}
+
+int64_t linear_blocks(int bits, int64_t m, int64_t rows) {
+  return grid_blocks(bits == 4 ? tile_grid<Lay<4, 8, 8>>(m, rows, true)
+                               : tile_grid<Lay<8, 8, 8>>(m, rows, true));
+}
+
+struct LinearCall {
+  const _Float16* x;
+  int64_t ldx, m;
+  const uint32_t* packed;
+  int64_t rows, cols;
+  const float *scales, *zeros;
+  int groupsize;
+  _Float16* y;
+  int64_t ldy;
+};
+
+template <int BITS, bool RELU, int TAIL, int A, int W>
+hipError_t launch_tile(const LinearCall& c, const Tail& tail, int splits, hipStream_t s) {
+  const int g = c.groupsize >= c.cols ? (int)c.cols : c.groupsize;
+  const int64_t ngroups = ceil_div(c.cols, g);
+  const int gk = (int)ceil_div(g, KG);  // chunks per group (a short last group ends at cols)
+  const int64_t nw = c.cols * BITS / 32;
+  const TileGrid grid = tile_grid<Lay<BITS, A, W>>(c.m, c.rows, TAIL == kStore);
+  hipLaunchKernelGGL((linear_kernel<BITS, RELU, TAIL, A, W>),
+                     dim3((unsigned)grid_blocks(grid), (unsigned)splits), dim3(64 * W), 0, s, c.x,
+                     c.ldx, c.m, c.packed, nw, c.rows, c.cols, c.scales, c.zeros, ngroups, gk, grid,
+                     c.y, c.ldy, tail);
   return hipGetLastError();
 }
 
-template <int BITS, int TAIL>
-hipError_t launch_bits(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed,
-                       int64_t rows, int64_t cols, const float* scales, const float* zeros,
-                       int groupsize, bool relu, const Tail& tail, _Float16* y, int64_t ldy,
+// The tile by the tokens: 64 tokens x 128 (64) outputs with four waves up to
+// 64 tokens, else 128 x 256 (128).
+template <bool RELU, int TAIL>
+hipError_t launch_tail(int bits, const LinearCall& c, const Tail& tail, int splits,
                        hipStream_t s) {
-  if (relu)
-    return launch_tail<BITS, true, TAIL>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize,
-                                         tail, y, ldy, s);
-  return launch_tail<BITS, false, TAIL>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize,
-                                        tail, y, ldy, s);
+  if (c.m <= 64)
+    return bits == 4 ? launch_tile<4, RELU, TAIL, 4, 4>(c, tail, splits, s)
+                     : launch_tile<8, RELU, TAIL, 4, 4>(c, tail, splits, s);
+  return bits == 4 ? launch_tile<4, RELU, TAIL, 8, 8>(c, tail, splits, s)
+                   : launch_tile<8, RELU, TAIL, 8, 8>(c, tail, splits, s);
+}
+
+int64_t tail_outputs(int bits, int64_t m) {  // outputs per tile
+  const int waves = m <= 64 ? 4 : 8;
+  return waves * (bits == 4 ? Geo<4>::WTN : Geo<8>::WTN);
 }
 
 }  // namespace
@@ -563,64 +691,83 @@ bool linear_forward_supported(int bits, int64_t m, int64_t rows, int64_t cols, i
          (groupsize % KG == 0 || groupsize >= cols) && ldx % 8 == 0 &&
          ldx < ((int64_t)1 << 23) && (reinterpret_cast<uintptr_t>(x) & 15) == 0 &&
          (reinterpret_cast<uintptr_t>(packed) & 15) == 0 &&
-         linear_blocks(bits, m, rows) * 64 * NWAVE <= (int64_t)UINT32_MAX;
+         linear_blocks(bits, m, rows) * 512 <= (int64_t)UINT32_MAX;
 }
 
 hipError_t launch_linear_forward(int bits, const _Float16* x, int64_t ldx, int64_t m,
                                  const uint32_t* packed, int64_t rows, int64_t cols,
                                  const float* scales, const float* zeros, int groupsize, bool relu,
                                  _Float16* y, int64_t ldy, hipStream_t s) {
+  const LinearCall c{x, ldx, m, packed, rows, cols, scales, zeros, groupsize, y, ldy};
+  const Tail t{};
   if (bits == 4)
-    return launch_bits<4, kStore>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize, relu,
-                                  Tail{}, y, ldy, s);
-  return launch_bits<8, kStore>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize, relu,
-                                Tail{}, y, ldy, s);
+    return relu ? launch_tile<4, true, kStore, 8, 8>(c, t, 1, s)
+                : launch_tile<4, false, kStore, 8, 8>(c, t, 1, s);
+  return relu ? launch_tile<8, true, kStore, 8, 8>(c, t, 1, s)
+              : launch_tile<8, false, kStore, 8, 8>(c, t, 1, s);
+}
+
+int linear_splits(int bits, int64_t m, int64_t rows, int64_t cols, int groupsize) {
+  const int64_t tiles = ceil_div(m, m <= 64 ? 64 : 128) * ceil_div(rows, tail_outputs(bits, m));
+  const int64_t groups = groupsize >= cols ? 1 : ceil_div(cols, groupsize);
+  int64_t s = 256 / tiles;
+  if (s > cols / KG / 2) s = cols / KG / 2;
+  if (s > groups) s = groups;  // a split takes whole groups
+  return s < 2 ? 1 : (int)s;
 }
 
 hipError_t launch_linear_forward_adapters(int bits, const _Float16* x, int64_t ldx, int64_t m,
                                           const uint32_t* packed, int64_t rows, int64_t cols,
                                           const float* scales, const float* zeros, int groupsize,
-                                          bool relu, const AdapterTile& ad, _Float16* y,
-                                          int64_t ldy, hipStream_t s) {
-  Tail tail{};
-  tail.ad = ad;
-  if (bits == 4)
-    return launch_bits<4, kAdapters>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize, relu,
-                                     tail, y, ldy, s);
-  return launch_bits<8, kAdapters>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize, relu,
-                                   tail, y, ldy, s);
+                                          bool relu, const AdapterTile& ad, float* sums,
+                                          _Float16* y, int64_t ldy, hipStream_t s) {
+  const LinearCall c{x, ldx, m, packed, rows, cols, scales, zeros, groupsize, y, ldy};
+  Tail t{};
+  t.ad = ad;
+  const int splits = linear_splits(bits, m, rows, cols, groupsize);
+  if (splits == 1)
+    return relu ? launch_tail<true, kAdapters>(bits, c, t, 1, s)
+                : launch_tail<false, kAdapters>(bits, c, t, 1, s);
+  t.sums = sums;
+  const hipError_t e = launch_tail<false, kSplit>(bits, c, t, splits, s);
+  if (e != hipSuccess) return e;
+  const dim3 grid((unsigned)m, (unsigned)ceil_div(rows, 256));
+  if (relu)
+    hipLaunchKernelGGL(linear_reduce_kernel<true>, grid, dim3(256), 0, s, sums, splits, m, rows, ad,
+                       y, ldy);
+  else
+    hipLaunchKernelGGL(linear_reduce_kernel<false>, grid, dim3(256), 0, s, sums, splits, m, rows,
+                       ad, y, ldy);
+  return hipGetLastError();
 }
 
-int64_t head_tiles(int bits, int64_t rows) {
-  return ceil_div(rows, bits == 4 ? Geo<4>::TN : Geo<8>::TN);
+int64_t head_tiles(int bits, int64_t m, int64_t rows) {
+  return ceil_div(rows, tail_outputs(bits, m));
 }
 
 hipError_t launch_head_partials(int bits, const _Float16* x, int64_t ldx, int64_t m,
                                 const uint32_t* packed, int64_t rows, int64_t cols,
                                 const float* scales, const float* zeros, int groupsize,
-                                float inv_t, float2* part, hipStream_t s) {
-  Tail tail{};
-  tail.inv_t = inv_t;
-  tail.part = part;
-  if (bits == 4)
-    return launch_tail<4, false, kPartials>(x, ldx, m, packed, rows, cols, scales, zeros,
-                                            groupsize, tail, nullptr, 0, s);
-  return launch_tail<8, false, kPartials>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize,
-                                          tail, nullptr, 0, s);
+                                const HeadTargets& tg, float2* part, float* zk, hipStream_t s) {
+  const LinearCall c{x, ldx, m, packed, rows, cols, scales, zeros, groupsize, nullptr, 0};
+  Tail t{};
+  t.inv_t = tg.inv_t;
+  t.part = part;
+  t.index = tg.index;
+  t.top = tg.top;
+  t.zk = zk;
+  return launch_tail<false, kPartials>(bits, c, t, 1, s);
 }
 
 hipError_t launch_head_probs(int bits, const _Float16* x, int64_t ldx, int64_t m,
                              const uint32_t* packed, int64_t rows, int64_t cols,
                              const float* scales, const float* zeros, int groupsize, float inv_t,
                              const float* lse, _Float16* P, int64_t ldp, hipStream_t s) {
-  Tail tail{};
-  tail.inv_t = inv_t;
-  tail.lse = lse;
-  if (bits == 4)
-    return launch_tail<4, false, kProbs>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize,
-                                         tail, P, ldp, s);
-  return launch_tail<8, false, kProbs>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize,
-                                       tail, P, ldp, s);
+  const LinearCall c{x, ldx, m, packed, rows, cols, scales, zeros, groupsize, P, ldp};
+  Tail t{};
+  t.inv_t = inv_t;
+  t.lse = lse;
+  return launch_tail<false, kProbs>(bits, c, t, 1, s);
 }
 
 }  // namespace gptq

@@ -87,8 +87,18 @@ HeadLayout head_layout(int64_t m, int64_t rows, int64_t cols) {
 }
 
 size_t partials_bytes(int64_t m, int64_t rows) {
-  // the 8-bit kernel's tiles of 128 outputs: the more of the two
-  return align_up((size_t)(head_tiles(8, rows) * m) * sizeof(float2));
+  // the 8-bit kernel's smaller tiles: the more of the two
+  return align_up((size_t)(head_tiles(8, m, rows) * m) * sizeof(float2));
+}
+
+// the tokens' v, and the split product's sums (8 bits: the smaller tiles may
+// split less)
+size_t forward_bytes(int64_t m, int64_t rows, int64_t cols, int rank) {
+  // groups of 128: the most splits a layer of these sizes can have
+  const int s4 = linear_splits(4, m, rows, cols, 128), s8 = linear_splits(8, m, rows, cols, 128);
+  const int splits = s4 > s8 ? s4 : s8;
+  return align_up((size_t)m * rank_pitch(rank) * sizeof(float)) +
+         (splits > 1 ? align_up((size_t)splits * m * rows * sizeof(float)) : 0);
 }
 
 bool sizes_ok(int64_t m, int64_t rows, int64_t cols, int bits, int groupsize) {
@@ -173,7 +183,7 @@ size_t gptq_adapters_workspace_bytes(int op, int64_t m, int64_t rows, int64_t co
   if ((count == 0) != (rank == 0)) return 0;
   switch (op) {
     case GPTQ_OP_FORWARD_ADAPTERS:
-      return align_up((size_t)m * rank_pitch(rank) * sizeof(float));
+      return m > 0 && rank > 0 ? forward_bytes(m, rows, cols, rank) : 0;
     case GPTQ_OP_BACKWARD:
       if (m == 0 || count > kMaxGradAdapters) return 0;
       return backward_layout(m, rows, cols, count, rank).total;
@@ -229,6 +239,7 @@ gptq_status gptq_linear_forward_adapters(const void* x, int64_t m, int64_t cols,
   GPTQ_TRY(launch_linear_forward_adapters(bits, reinterpret_cast<const _Float16*>(x), ldx, m,
                                           packed, rows, cols, scales, zeros, groupsize, relu == 1,
                                           forward_tile(ad, rows, v),
+                                          v + align_up(m * rank_pitch(ad->rank) * 4) / 4,
                                           reinterpret_cast<_Float16*>(y), ldy, s));
   return GPTQ_OK;
 }
@@ -377,9 +388,8 @@ gptq_status head_forward(const void* h, int64_t m, int64_t cols, int64_t ldh,
   const _Float16* x = reinterpret_cast<const _Float16*>(h);
   float2* part = reinterpret_cast<float2*>(workspace);
   GPTQ_TRY(launch_head_partials(bits, x, ldh, m, packed, rows, cols, scales, zeros, groupsize,
-                                tg.inv_t, part, s));
-  GPTQ_TRY(launch_head_finish(bits, x, ldh, m, packed, rows, cols, scales, zeros, groupsize, tg,
-                              part, head_tiles(bits, rows), loss, lse, zk, s));
+                                tg, part, zk, s));
+  GPTQ_TRY(launch_head_finish(m, rows, tg, part, head_tiles(bits, m, rows), loss, lse, zk, s));
   return GPTQ_OK;
 }
 
