@@ -71,18 +71,22 @@ __global__ __launch_bounds__(256) void shrink_rows_kernel(ShrinkJob job, int64_t
 }
 
 // v for 16 tokens per workgroup on v_mfma_f32_16x16x32_f16 (tokens x rank
-// tiles of 16), the four waves taking every fourth run of 32 of K and their
+// tiles of 16), the eight waves taking every eighth run of 32 of K and their
 // sums added in wave order.  One pass per adapter found among the 16 tokens.
-template <bool VEC, int NB>
-__global__ __launch_bounds__(256) void shrink_tile_kernel(ShrinkJob j0, ShrinkJob j1, int64_t m) {
-  __shared__ float red[4][16][16 * NB + 1];
+// Bound by the read of x: U runs are in flight per wave.
+constexpr int kShrinkWaves = 8;
+template <bool VEC, int NB, int U>
+__global__ __launch_bounds__(64 * kShrinkWaves) void shrink_tile_kernel(ShrinkJob j0, ShrinkJob j1,
+                                                                        int64_t m) {
+  constexpr int W = kShrinkWaves;
+  __shared__ float red[W][16][16 * NB + 1];
   const ShrinkJob& job = blockIdx.y == 0 ? j0 : j1;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, kg = lane >> 4;
   const int64_t t0 = (int64_t)blockIdx.x * 16;
   const int id = t0 + li < m ? valid_id(job.index, t0 + li, job.count) : -1;
   const _Float16* x = job.x + min(t0 + li, m - 1) * job.ldx;
   // zeros where a token has no adapter, and behind the rank
-  for (int o = tid; o < 16 * job.ldv; o += 256) {
+  for (int o = tid; o < 16 * job.ldv; o += 64 * W) {
     const int tok = o / job.ldv, j = o % job.ldv;
     if (t0 + tok < m && (j >= job.rank || valid_id(job.index, t0 + tok, job.count) < 0))
       job.v[(t0 + tok) * job.ldv + j] = 0.f;
@@ -93,19 +97,29 @@ __global__ __launch_bounds__(256) void shrink_tile_kernel(ShrinkJob j0, ShrinkJo
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) next = min(next, __shfl_xor(next, o, 64));
     cur = __builtin_amdgcn_readfirstlane(next);
-    if (cur == 0x7fffffff) break;  // the same in all four waves
+    if (cur == 0x7fffffff) break;  // the same in all the waves
     const _Float16* down = job.down + cur * job.stride;
     f32x4 acc[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int64_t k = 32 * wave + 8 * kg; k - 8 * kg < job.K; k += 128) {
-      const half8 xv = load8<VEC>(x, k, job.K);
+    for (int64_t k0 = 32 * wave; k0 < job.K; k0 += 32 * W * U) {
+      half8 xv[U], dv[U][NB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        half8 dv = {};
-        if (16 * b + li < job.rank) dv = load8<VEC>(down + (16 * b + li) * job.ldd, k, job.K);
-        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv, dv, acc[b], 0, 0, 0);
+      for (int u = 0; u < U; ++u) {
+        const int64_t k = k0 + 32 * W * u + 8 * kg;
+        xv[u] = load8<VEC>(x, k, job.K);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const int j = 16 * b + li;  // a row of the adapter, zero behind the rank
+          dv[u][b] = load8<VEC>(down + min(j, job.rank - 1) * job.ldd, j < job.rank ? k : job.K,
+                                job.K);
+        }
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[u], dv[u][b], acc[b], 0, 0, 0);
     }
     __syncthreads();  // the previous turn's reads of red
 #pragma unroll
@@ -114,11 +128,14 @@ __global__ __launch_bounds__(256) void shrink_tile_kernel(ShrinkJob j0, ShrinkJo
       for (int i = 0; i < 4; ++i) red[wave][4 * kg + i][16 * b + li] = acc[b][i];
     __syncthreads();
     const float s = job.scaling[cur];
-    for (int o = tid; o < 16 * 16 * NB; o += 256) {
+    for (int o = tid; o < 16 * 16 * NB; o += 64 * W) {
       const int tok = o / (16 * NB), j = o % (16 * NB);
-      if (t0 + tok < m && job.index[t0 + tok] == cur && j < job.rank)
-        job.v[(t0 + tok) * job.ldv + j] =
-            s * ((red[0][tok][j] + red[1][tok][j]) + (red[2][tok][j] + red[3][tok][j]));
+      if (t0 + tok < m && job.index[t0 + tok] == cur && j < job.rank) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) sum += red[w][tok][j];
+        job.v[(t0 + tok) * job.ldv + j] = s * sum;
+      }
     }
   }
 }
@@ -277,8 +294,10 @@ bool vec_job(const ShrinkJob& j) { return vec_ok(j.x, j.ldx, j.K) && vec_ok(j.do
 
 template <bool VEC, int NB>
 void shrink_tiles(const ShrinkJob& j0, const ShrinkJob* j1, int64_t m, hipStream_t s) {
-  hipLaunchKernelGGL((shrink_tile_kernel<VEC, NB>), dim3((unsigned)ceil_div(m, 16), j1 ? 2 : 1),
-                     dim3(256), 0, s, j0, j1 ? *j1 : j0, m);
+  constexpr int U = !VEC ? 1 : NB <= 2 ? 4 : 2;
+  hipLaunchKernelGGL((shrink_tile_kernel<VEC, NB, U>),
+                     dim3((unsigned)ceil_div(m, 16), j1 ? 2 : 1), dim3(64 * kShrinkWaves), 0, s, j0,
+                     j1 ? *j1 : j0, m);
 }
 
 }  // namespace

@@ -154,11 +154,17 @@ hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t s);
 constexpr int kMaxRank = 128;
 // the adapters' part of a product (adapters_dev.h)
 struct AdapterTile;
-hipError_t launch_dequant_gemv_adapters(const _Float16* x, int64_t ldx, int64_t m,
-                                        const uint32_t* packed, int bits, int64_t rows,
-                                        int64_t cols, const float* scales, const float* zeros,
-                                        int groupsize, const int* g_idx, const AdapterTile& ad,
-                                        float* y, int64_t ldy, hipStream_t s);
+hipError_t launch_decode_adapters(const _Float16* x, int64_t ldx, int64_t m,
+                                  const uint32_t* packed, int bits, int64_t rows, int64_t cols,
+                                  const float* scales, const float* zeros, int groupsize,
+                                  const int* g_idx, const AdapterTile& ad, float* y, int64_t ldy,
+                                  hipStream_t s);
+bool gemv_fast_ok(int bits, int64_t cols, int groupsize, const int* g_idx,
+                  const uint32_t* packed);
+hipError_t launch_gemv_adapters(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed,
+                                int bits, int64_t rows, int64_t cols, const float* scales,
+                                const float* zeros, int groupsize, const AdapterTile& ad, float* y,
+                                int64_t ldy, hipStream_t s);
 hipError_t launch_linear_forward_adapters(int bits, const _Float16* x, int64_t ldx, int64_t m,
                                           const uint32_t* packed, int64_t rows, int64_t cols,
                                           const float* scales, const float* zeros, int groupsize,

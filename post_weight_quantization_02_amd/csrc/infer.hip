@@ -47,39 +47,16 @@ __global__ __launch_bounds__(256) void pack_codes_kernel(const uint8_t* __restri
   out[r * nw + w] = v;
 }
 
-// One lane's share of sum_j v[t][j] up[a][j][r], a = index[t] (the 64 lanes'
-// shares add up to it); 0 for a token without an adapter.
-__device__ inline float adapter_share(const AdapterTile& ad, int64_t t, int64_t r, int lane) {
-  const int a = ad.index[t];
-  if (a < 0 || a >= ad.count) return 0.f;
-  const _Float16* up = ad.up + a * ad.stride + r * ad.ns;
-  float sum = 0.f;
-  for (int j = lane; j < ad.rank; j += 64)
-    sum = __builtin_fmaf(ad.v[t * ad.ldv + j], (float)up[j * ad.js], sum);
-  return sum;
-}
-
-// the adapters of the tokens from t0 on
-AdapterTile from_token(const AdapterTile& ad, int64_t t0) {
-  AdapterTile b = ad;
-  if (b.v != nullptr) {
-    b.v += t0 * b.ldv;
-    b.index += t0;
-  }
-  return b;
-}
-
 constexpr int kGemvRows = 4;   // output rows per wave
 constexpr int kGemvUnroll = 4; // words per lane in flight per row
 
-// y[t][r] = sum_c x[t][c] * W_hat[r][c] for t < m <= MT (AD: plus the
-// tokens' adapters).
-template <int BITS, int MT, bool AD>
+// y[t][r] = sum_c x[t][c] * W_hat[r][c] for t < m <= MT.
+template <int BITS, int MT>
 __global__ __launch_bounds__(256) void dequant_gemv_kernel(
     const _Float16* __restrict__ x, int64_t ldx, int m, const uint32_t* __restrict__ packed,
     int64_t nw, int64_t rows, int64_t cols, const float* __restrict__ scales,
     const float* __restrict__ zeros, int64_t ngroups, int groupsize, const int* __restrict__ g_idx,
-    float* __restrict__ y, int64_t ldy, AdapterTile ad) {
+    float* __restrict__ y, int64_t ldy) {
   constexpr int K = 32 / BITS;
   constexpr uint32_t MASK = (1u << BITS) - 1u;
   constexpr int R = kGemvRows;
@@ -150,13 +127,6 @@ __global__ __launch_bounds__(256) void dequant_gemv_kernel(
       }
     }
   }
-  if constexpr (AD) {
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-        if (t < m) acc[i][t] += adapter_share(ad, t, rr[i], lane);
-  }
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -195,6 +165,18 @@ __device__ inline void unpack_word(uint32_t w, float (&q)[32 / BITS]) {
   }
 }
 
+// One lane's share of sum_j v[t][j] up[a][j][r], a = index[t] (the 64 lanes'
+// shares add up to it); 0 for a token without an adapter.
+__device__ inline float adapter_share(const AdapterTile& ad, int64_t t, int64_t r, int lane) {
+  const int a = ad.index[t];
+  if (a < 0 || a >= ad.count) return 0.f;
+  const _Float16* up = ad.up + a * ad.stride + r * ad.ns;
+  float sum = 0.f;
+  for (int j = lane; j < ad.rank; j += 64)
+    sum = __builtin_fmaf(ad.v[t * ad.ldv + j], (float)up[j * ad.js], sum);
+  return sum;
+}
+
 // Fast path for 2, 4 and 8 bits when every 4-word run of a row (4K columns)
 // lies in one group and no g_idx is given.  x (MT tokens) is staged in LDS as
 // fp16.  A lane reads 4 words of each of its R rows with one 16-byte load
@@ -203,6 +185,7 @@ __device__ inline void unpack_word(uint32_t w, float (&q)[32 / BITS]) {
 // equals sum x (q - z) s.  Rounding: the products x * q are exact in fp32,
 // so each output's error is at most
 // (4K + ceil(runs / 64) + 8) * 2^-24 * sum_c |x_c| (|q_c| + |z_g|) s_g.
+// AD: a token's low-rank adapter joins the lanes' sums before they are added.
 template <int BITS, int MT, int R, bool XD, bool AD>
 __global__ __launch_bounds__(256) void dequant_gemv_fast_kernel(
     const _Float16* __restrict__ x, int64_t ldx, int m, const uint32_t* __restrict__ packed,
@@ -466,12 +449,12 @@ __device__ inline half8 codes4_f16(uint32_t w) {
   return r;
 }
 
-template <int TT, bool AD>  // token tiles of 16 per pass
+template <int TT>  // token tiles of 16 per pass
 __global__ __launch_bounds__(256) void dequant_gemm_mfma_kernel(
     const _Float16* __restrict__ x, int64_t ldx, int m, const uint32_t* __restrict__ packed,
     int64_t nw, int64_t rows, int64_t cols, const float* __restrict__ scales,
     const float* __restrict__ zeros, int64_t ngroups, int groupsize, float* __restrict__ y,
-    int64_t ldy, AdapterTile ad) {
+    int64_t ldy) {
   __shared__ float part[4][TT * 16][17];  // per-wave partial tiles [wave][token][row]
   const int tid = threadIdx.x;
   const int lane = tid & 63, wave = tid >> 6;
@@ -551,19 +534,7 @@ __global__ __launch_bounds__(256) void dequant_gemm_mfma_kernel(
   __syncthreads();
   for (int o = tid; o < TT * 256; o += 256) {
     const int tok = o >> 4, rw = o & 15;
-    float v = (part[0][tok][rw] + part[1][tok][rw]) + (part[2][tok][rw] + part[3][tok][rw]);
-    if constexpr (AD) {
-      if (tok < m && r0 + rw < rows) {
-        const int a = ad.index[tok];
-        if (a >= 0 && a < ad.count) {
-          const _Float16* up = ad.up + a * ad.stride + (r0 + rw) * ad.ns;
-          float low = 0.f;
-          for (int j = 0; j < ad.rank; ++j)
-            low = __builtin_fmaf(ad.v[(int64_t)tok * ad.ldv + j], (float)up[j * ad.js], low);
-          v += low;
-        }
-      }
-    }
+    const float v = (part[0][tok][rw] + part[1][tok][rw]) + (part[2][tok][rw] + part[3][tok][rw]);
     if (tok < m && r0 + rw < rows) y[(int64_t)tok * ldy + r0 + rw] = v;
   }
 }
@@ -576,24 +547,23 @@ bool dequant_mfma_ok(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* 
          (reinterpret_cast<uintptr_t>(packed) & 15) == 0;
 }
 
-template <bool AD>
 hipError_t launch_dequant_mfma(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed,
                                int64_t rows, int64_t cols, const float* scales,
-                               const float* zeros, int groupsize, const AdapterTile& ad, float* y,
-                               int64_t ldy, hipStream_t s) {
+                               const float* zeros, int groupsize, float* y, int64_t ldy,
+                               hipStream_t s) {
   const int64_t nw = packed_words(cols, 4);
   const int64_t ngroups = ceil_div(cols, groupsize);
   const dim3 grid((unsigned)ceil_div(rows, 16));
   for (int64_t t0 = 0; t0 < m; t0 += 32) {
     const int mt = (int)((m - t0 < 32) ? m - t0 : 32);
     if (mt > 16)
-      hipLaunchKernelGGL((dequant_gemm_mfma_kernel<2, AD>), grid, dim3(256), 0, s, x + t0 * ldx, ldx, mt,
+      hipLaunchKernelGGL(dequant_gemm_mfma_kernel<2>, grid, dim3(256), 0, s, x + t0 * ldx, ldx, mt,
                          packed, nw, rows, cols, scales, zeros, ngroups, groupsize, y + t0 * ldy,
-                         ldy, from_token(ad, t0));
+                         ldy);
     else
-      hipLaunchKernelGGL((dequant_gemm_mfma_kernel<1, AD>), grid, dim3(256), 0, s, x + t0 * ldx, ldx, mt,
+      hipLaunchKernelGGL(dequant_gemm_mfma_kernel<1>, grid, dim3(256), 0, s, x + t0 * ldx, ldx, mt,
                          packed, nw, rows, cols, scales, zeros, ngroups, groupsize, y + t0 * ldy,
-                         ldy, from_token(ad, t0));
+                         ldy);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -601,6 +571,16 @@ hipError_t launch_dequant_mfma(const _Float16* x, int64_t ldx, int64_t m, const 
 }
 
 constexpr int64_t kGemvLds = 64 * 1024;  // x staging limit of the fast path
+
+// the adapters of the tokens from t0 on (ad.v NULL: none)
+AdapterTile from_token(const AdapterTile& ad, int64_t t0) {
+  AdapterTile b = ad;
+  if (b.v != nullptr) {
+    b.v += t0 * b.ldv;
+    b.index += t0;
+  }
+  return b;
+}
 
 template <int BITS, int R, bool AD>
 hipError_t launch_gemv_fast_direct(const _Float16* x, int64_t ldx, int64_t m,
@@ -650,28 +630,25 @@ hipError_t launch_gemv_fast(const _Float16* x, int64_t ldx, int64_t m, const uin
   return hipSuccess;
 }
 
-template <int BITS, bool AD>
+template <int BITS>
 hipError_t launch_gemv_bits(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed,
                             int64_t nw, int64_t rows, int64_t cols, const float* scales,
                             const float* zeros, int64_t ngroups, int groupsize, const int* g_idx,
-                            const AdapterTile& ad, float* y, int64_t ldy, hipStream_t s) {
+                            float* y, int64_t ldy, hipStream_t s) {
   const dim3 grid((unsigned)ceil_div(rows, 4 * kGemvRows));
   for (int64_t t0 = 0; t0 < m; t0 += 4) {
     const int mt = (int)((m - t0 < 4) ? m - t0 : 4);
     const _Float16* xt = x + t0 * ldx;
     float* yt = y + t0 * ldy;
     if (mt == 1)
-      hipLaunchKernelGGL((dequant_gemv_kernel<BITS, 1, AD>), grid, dim3(256), 0, s, xt, ldx, mt,
-                         packed, nw, rows, cols, scales, zeros, ngroups, groupsize, g_idx, yt, ldy,
-                         from_token(ad, t0));
+      hipLaunchKernelGGL((dequant_gemv_kernel<BITS, 1>), grid, dim3(256), 0, s, xt, ldx, mt,
+                         packed, nw, rows, cols, scales, zeros, ngroups, groupsize, g_idx, yt, ldy);
     else if (mt == 2)
-      hipLaunchKernelGGL((dequant_gemv_kernel<BITS, 2, AD>), grid, dim3(256), 0, s, xt, ldx, mt,
-                         packed, nw, rows, cols, scales, zeros, ngroups, groupsize, g_idx, yt, ldy,
-                         from_token(ad, t0));
+      hipLaunchKernelGGL((dequant_gemv_kernel<BITS, 2>), grid, dim3(256), 0, s, xt, ldx, mt,
+                         packed, nw, rows, cols, scales, zeros, ngroups, groupsize, g_idx, yt, ldy);
     else
-      hipLaunchKernelGGL((dequant_gemv_kernel<BITS, 4, AD>), grid, dim3(256), 0, s, xt, ldx, mt,
-                         packed, nw, rows, cols, scales, zeros, ngroups, groupsize, g_idx, yt, ldy,
-                         from_token(ad, t0));
+      hipLaunchKernelGGL((dequant_gemv_kernel<BITS, 4>), grid, dim3(256), 0, s, xt, ldx, mt,
+                         packed, nw, rows, cols, scales, zeros, ngroups, groupsize, g_idx, yt, ldy);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -682,59 +659,49 @@ hipError_t launch_gemv_bits(const _Float16* x, int64_t ldx, int64_t m, const uin
 template <bool AD>
 hipError_t launch_gemv_any(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed,
                            int bits, int64_t rows, int64_t cols, const float* scales,
-                           const float* zeros, int groupsize, const int* g_idx,
-                           const AdapterTile& ad, float* y, int64_t ldy, hipStream_t s) {
+                           const float* zeros, int groupsize, const AdapterTile& ad, float* y,
+                           int64_t ldy, hipStream_t s) {
   const int64_t nw = packed_words(cols, bits);
   const int64_t ngroups = ceil_div(cols, groupsize);
-  // two tokens or more, 4 bits, whole 128-column chunks inside groups: MFMA,
-  // the weights read once per 32 tokens
-  if (dequant_mfma_ok(x, ldx, m, packed, bits, cols, groupsize, g_idx))
-    return launch_dequant_mfma<AD>(x, ldx, m, packed, rows, cols, scales, zeros, groupsize, ad, y, ldy,
-                                   s);
-  // fast path: 2, 4 or 8 bits, whole 4-word runs inside groups, no g_idx,
-  // 16-byte aligned rows, x of at least one token fits the LDS staging
-  if ((bits == 2 || bits == 4 || bits == 8) && g_idx == nullptr && nw % 4 == 0 &&
-      groupsize % (4 * (32 / bits)) == 0 && (reinterpret_cast<uintptr_t>(packed) & 15) == 0) {
-    const int64_t row_bytes = nw * (32 / bits) * 2;
-    const int maxmt = (int)((kGemvLds / row_bytes >= 4) ? 4 : (kGemvLds / row_bytes >= 2) ? 2
-                                                                                          : 1);
-    if (row_bytes <= kGemvLds) {
-      // two rows per wave (measured against one and four: 1.78 ms per
-      // decode step against 1.86 and 1.81 at one token)
-      if (bits == 2)
-        return launch_gemv_fast<2, 2, AD>(x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups,
+  const int64_t row_bytes = nw * (32 / bits) * 2;
+  const int maxmt = (int)((kGemvLds / row_bytes >= 4) ? 4 : (kGemvLds / row_bytes >= 2) ? 2 : 1);
+  // two rows per wave (measured against one and four: 1.78 ms per
+  // decode step against 1.86 and 1.81 at one token)
+  if (bits == 2)
+    return launch_gemv_fast<2, 2, AD>(x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups,
                                       groupsize, ad, y, ldy, maxmt, s);
-      // one token, whole 32-column runs, aligned x rows: x loaded directly
-      if (bits == 4 && m == 1 && cols % 32 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0)
-        return launch_gemv_fast_direct<4, 2, AD>(x, ldx, m, packed, nw, rows, cols, scales, zeros,
+  // one token, whole 32-column runs, aligned x rows: x loaded directly
+  if (bits == 4 && m == 1 && cols % 32 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0)
+    return launch_gemv_fast_direct<4, 2, AD>(x, ldx, m, packed, nw, rows, cols, scales, zeros,
                                              ngroups, groupsize, ad, y, ldy, s);
-      if (bits == 4)
-        return launch_gemv_fast<4, 2, AD>(x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups,
+  if (bits == 4)
+    return launch_gemv_fast<4, 2, AD>(x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups,
                                       groupsize, ad, y, ldy, maxmt, s);
-      return launch_gemv_fast<8, 2, AD>(x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups,
+  return launch_gemv_fast<8, 2, AD>(x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups,
                                     groupsize, ad, y, ldy, maxmt, s);
-    }
-  }
-  switch (bits) {
-#define GPTQ_GEMV(B) \
-  case B:            \
-    return launch_gemv_bits<B, AD>(x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups, \
-                               groupsize, g_idx, ad, y, ldy, s);
-    GPTQ_GEMV(2)
-    GPTQ_GEMV(3)
-    GPTQ_GEMV(4)
-    GPTQ_GEMV(5)
-    GPTQ_GEMV(6)
-    GPTQ_GEMV(7)
-    GPTQ_GEMV(8)
-#undef GPTQ_GEMV
-    default: return hipErrorInvalidValue;
-  }
 }
 
 }  // namespace
 
 int64_t packed_words(int64_t cols, int bits) { return ceil_div(cols, 32 / bits); }
+
+// the fast path: 2, 4 or 8 bits, whole 4-word runs inside groups, no g_idx,
+// 16-byte aligned rows, x of at least one token fits the LDS staging
+bool gemv_fast_ok(int bits, int64_t cols, int groupsize, const int* g_idx,
+                  const uint32_t* packed) {
+  const int64_t nw = packed_words(cols, bits);
+  return (bits == 2 || bits == 4 || bits == 8) && g_idx == nullptr && nw % 4 == 0 &&
+         groupsize % (4 * (32 / bits)) == 0 && (reinterpret_cast<uintptr_t>(packed) & 15) == 0 &&
+         nw * (32 / bits) * 2 <= kGemvLds;
+}
+
+hipError_t launch_gemv_adapters(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed,
+                                int bits, int64_t rows, int64_t cols, const float* scales,
+                                const float* zeros, int groupsize, const AdapterTile& ad, float* y,
+                                int64_t ldy, hipStream_t s) {
+  return launch_gemv_any<true>(x, ldx, m, packed, bits, rows, cols, scales, zeros, groupsize, ad, y,
+                               ldy, s);
+}
 
 hipError_t launch_pack_codes(const uint8_t* codes, int64_t rows, int64_t cols, int bits,
                              uint32_t* packed, hipStream_t s) {
@@ -749,17 +716,30 @@ hipError_t launch_dequant_gemv(const _Float16* x, int64_t ldx, int64_t m, const 
                                int bits, int64_t rows, int64_t cols, const float* scales,
                                const float* zeros, int groupsize, const int* g_idx, float* y,
                                int64_t ldy, hipStream_t s) {
-  return launch_gemv_any<false>(x, ldx, m, packed, bits, rows, cols, scales, zeros, groupsize,
-                                g_idx, AdapterTile{}, y, ldy, s);
-}
-
-hipError_t launch_dequant_gemv_adapters(const _Float16* x, int64_t ldx, int64_t m,
-                                        const uint32_t* packed, int bits, int64_t rows,
-                                        int64_t cols, const float* scales, const float* zeros,
-                                        int groupsize, const int* g_idx, const AdapterTile& ad,
-                                        float* y, int64_t ldy, hipStream_t s) {
-  return launch_gemv_any<true>(x, ldx, m, packed, bits, rows, cols, scales, zeros, groupsize,
-                               g_idx, ad, y, ldy, s);
+  const int64_t nw = packed_words(cols, bits);
+  const int64_t ngroups = ceil_div(cols, groupsize);
+  // two tokens or more, 4 bits, whole 128-column chunks inside groups: MFMA,
+  // the weights read once per 32 tokens
+  if (dequant_mfma_ok(x, ldx, m, packed, bits, cols, groupsize, g_idx))
+    return launch_dequant_mfma(x, ldx, m, packed, rows, cols, scales, zeros, groupsize, y, ldy, s);
+  if (gemv_fast_ok(bits, cols, groupsize, g_idx, packed))
+    return launch_gemv_any<false>(x, ldx, m, packed, bits, rows, cols, scales, zeros, groupsize,
+                                  AdapterTile{}, y, ldy, s);
+  switch (bits) {
+#define GPTQ_GEMV(B) \
+  case B:            \
+    return launch_gemv_bits<B>(x, ldx, m, packed, nw, rows, cols, scales, zeros, ngroups, \
+                               groupsize, g_idx, y, ldy, s);
+    GPTQ_GEMV(2)
+    GPTQ_GEMV(3)
+    GPTQ_GEMV(4)
+    GPTQ_GEMV(5)
+    GPTQ_GEMV(6)
+    GPTQ_GEMV(7)
+    GPTQ_GEMV(8)
+#undef GPTQ_GEMV
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace gptq

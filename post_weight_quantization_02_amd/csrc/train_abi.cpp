@@ -16,7 +16,6 @@ constexpr int64_t kMaxDim = 1 << 20;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 constexpr int64_t kMaxTokens = (int64_t)1 << 23;  // token lists hold ints, grids 2^16 chunks
 constexpr int64_t kMaxAdapters = 1 << 20;
-constexpr int64_t kRowsKernelTokens = 64;  // tokens up to which each has a workgroup of its own
 constexpr int64_t kHeadTokens = 8192;      // tokens per pass of the loss's gradient
 
 inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
@@ -161,8 +160,11 @@ AdapterTile forward_tile(const gptq_adapters* ad, int64_t rows, const float* v) 
   return t;
 }
 
+// A few tokens have workgroups of their own: 16-token tiles leave CUs idle.
+// Per token that reads every adapter row again (rank + rank / 4 rows of K from
+// the L2), so the limit falls with the rank.
 hipError_t shrink(const ShrinkJob& job, int64_t m, hipStream_t s) {
-  if (m <= kRowsKernelTokens) return launch_shrink_rows(job, m, s);
+  if (m * job.ldv <= 8192) return launch_shrink_rows(job, m, s);
   return launch_shrink_tiles(job, nullptr, m, s);
 }
 
@@ -210,9 +212,9 @@ gptq_status gptq_dequant_gemm_adapters(const void* x, int64_t m, int64_t cols, i
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   float* v = reinterpret_cast<float*>(workspace);
   GPTQ_TRY(shrink(forward_job(ad, x, ldx, cols, v), m, s));
-  GPTQ_TRY(launch_dequant_gemv_adapters(reinterpret_cast<const _Float16*>(x), ldx, m, packed, bits,
-                                        rows, cols, scales, zeros, groupsize, g_idx,
-                                        forward_tile(ad, rows, v), y, ldy, s));
+  GPTQ_TRY(launch_decode_adapters(reinterpret_cast<const _Float16*>(x), ldx, m, packed, bits, rows,
+                                  cols, scales, zeros, groupsize, g_idx, forward_tile(ad, rows, v),
+                                  y, ldy, s));
   return GPTQ_OK;
 }
 
