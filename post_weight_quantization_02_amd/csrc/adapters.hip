@@ -28,6 +28,18 @@ __device__ inline int valid_id(const int* index, int64_t t, int count) {
   return (d >= 0 && d < count) ? d : -1;
 }
 
+// Token t's row into its place in xp (see launch_pack_x).
+__device__ inline void pack_row(const _Float16* x, int64_t t, int64_t K, _Float16* xp) {
+  for (int64_t p = threadIdx.x; p < K / 8; p += 256)  // p: chunk, step, piece
+    *reinterpret_cast<half8*>(xp + ((t / 16) * (K / 8) + p) * 128 + (t % 16) * 8) =
+        *reinterpret_cast<const half8*>(x + 8 * p);
+}
+
+__global__ __launch_bounds__(256) void pack_x_kernel(const _Float16* __restrict__ x, int64_t ldx,
+                                                     int64_t K, _Float16* __restrict__ xp) {
+  pack_row(x + (int64_t)blockIdx.x * ldx, blockIdx.x, K, xp);
+}
+
 // v[t][j] for one token and four j per workgroup: a few tokens, each with an
 // adapter of its own (decode).  Bound by the read of the adapters' rows.
 template <bool VEC>
@@ -37,6 +49,7 @@ __global__ __launch_bounds__(256) void shrink_rows_kernel(ShrinkJob job, int64_t
   const int j0 = 4 * blockIdx.y;
   const int a = valid_id(job.index, t, job.count);
   float* out = job.v + t * job.ldv + j0;
+  if (job.xp != nullptr && blockIdx.y == 0) pack_row(job.x + t * job.ldx, t, job.K, job.xp);
   if (a < 0) {  // the whole workgroup
     if (threadIdx.x < 4) out[threadIdx.x] = 0.f;
     return;
@@ -301,6 +314,12 @@ void shrink_tiles(const ShrinkJob& j0, const ShrinkJob* j1, int64_t m, hipStream
 }
 
 }  // namespace
+
+hipError_t launch_pack_x(const _Float16* x, int64_t ldx, int64_t m, int64_t K, _Float16* xp,
+                         hipStream_t s) {
+  hipLaunchKernelGGL(pack_x_kernel, dim3((unsigned)m), dim3(256), 0, s, x, ldx, K, xp);
+  return hipGetLastError();
+}
 
 hipError_t launch_shrink_rows(const ShrinkJob& job, int64_t m, hipStream_t s) {
   const dim3 grid((unsigned)m, (unsigned)(job.ldv / 4));

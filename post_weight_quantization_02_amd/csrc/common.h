@@ -123,11 +123,16 @@ struct ShrinkJob {
   int count, rank;
   float* v;
   int ldv;
+  _Float16* xp;  // launch_shrink_rows: if given, x also laid out as launch_pack_x does
 };
 // one workgroup per token and four j (a few tokens), or 16-token tiles of one
 // or two jobs of the same ldv
 hipError_t launch_shrink_rows(const ShrinkJob& job, int64_t m, hipStream_t s);
 hipError_t launch_shrink_tiles(const ShrinkJob& j0, const ShrinkJob* j1, int64_t m, hipStream_t s);
+// xp: x (K % 128 == 0, 16-byte aligned rows) in 16-byte pieces of 8 columns:
+// [16-token tile][128-column chunk][32-column step][8-column piece][token]
+hipError_t launch_pack_x(const _Float16* x, int64_t ldx, int64_t m, int64_t K, _Float16* xp,
+                         hipStream_t s);
 hipError_t launch_transpose_up(const _Float16* B, int64_t count, int64_t rows, int rank,
                                int64_t ldt, _Float16* Bt, hipStream_t s);
 // out[a] = sum over the tokens t of adapter a of left[t][j] right[t][c]
@@ -154,7 +159,10 @@ hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t s);
 constexpr int kMaxRank = 128;
 // the adapters' part of a product (adapters_dev.h)
 struct AdapterTile;
-hipError_t launch_decode_adapters(const _Float16* x, int64_t ldx, int64_t m,
+// xp: x as launch_shrink_rows or launch_pack_x laid it out, where decode_mfma_ok
+bool decode_mfma_ok(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed, int bits,
+                    int64_t cols, int groupsize, const int* g_idx);
+hipError_t launch_decode_adapters(const _Float16* x, const _Float16* xp, int64_t ldx, int64_t m,
                                   const uint32_t* packed, int bits, int64_t rows, int64_t cols,
                                   const float* scales, const float* zeros, int groupsize,
                                   const int* g_idx, const AdapterTile& ad, float* y, int64_t ldy,
@@ -173,13 +181,16 @@ hipError_t launch_linear_forward_adapters(int bits, const _Float16* x, int64_t l
 // splits of the input columns when the tiles leave CUs idle (1: none); their
 // fp32 sums, splits x m x rows, go to the workspace
 int linear_splits(int bits, int64_t m, int64_t rows, int64_t cols, int groupsize);
-// the transposed weights and the products with them
+// the transposed weights, cols x kp (kp >= rows a multiple of kKPad, zeros
+// behind the rows) with row pitch ldt, and the products with them
 constexpr int kKPad = 64;  // K of the fp16 product, padded with zeros
 hipError_t launch_dequant_transposed(const uint32_t* packed, int bits, int64_t rows, int64_t cols,
                                      const float* scales, const float* zeros, int groupsize,
-                                     const int* g_idx, int64_t ldt, _Float16* Wt, hipStream_t s);
-hipError_t launch_pad_rows(const _Float16* src, int64_t lds, int64_t m, int64_t K, int64_t ldd,
-                           _Float16* dst, hipStream_t s);
+                                     const int* g_idx, int64_t kp, int64_t ldt, _Float16* Wt,
+                                     hipStream_t s);
+// dst[t][0 .. kp) = src[t][0 .. K) and zeros, row pitch ldd
+hipError_t launch_pad_rows(const _Float16* src, int64_t lds, int64_t m, int64_t K, int64_t kp,
+                           int64_t ldd, _Float16* dst, hipStream_t s);
 // C = A B^T, A m x K, B n x K (K % kKPad == 0, 16-byte aligned rows)
 hipError_t launch_gemm_nt_f16(const _Float16* A, int64_t lda, int64_t m, const _Float16* B,
                               int64_t ldb, int64_t n, int64_t K, const AdapterTile* ad,

@@ -48,14 +48,18 @@ __device__ inline float low_rank(const AdapterTile& ad, int64_t t, int64_t r) {
 // zero.
 //
 // x comes from the L2 for every workgroup (8 times the weights' bytes at 32
-// tokens), so its loads decide: step q reads 64 adjacent bytes of 16 rows,
-// lane group kg columns 32 q + 8 kg.. of the chunk.  (Lane group kg on columns
-// 32 kg.., the order of the packed words, puts every lane on a 64-byte
-// segment of its own and the address unit takes the lanes one by one: 53 us
-// against 14 us at 11008 x 4096, 32 tokens.)  The 4-bit words arrive as one
+// tokens), so it is laid out first (with v) as the fragments read it: 1 KB per
+// instruction, where rows of x would put 16 lanes' 64-byte pieces on one L2
+// channel (8 KB apart at 4096 columns; 31 against 26 us at 11008 x 4096, 32
+// tokens), and the packed words' own order, lane group kg on columns 32 kg..,
+// every lane on a segment of its own (37 us).  The 4-bit words arrive as one
 // 16-byte load per lane, word j of lane group kg, and two exchanges between
-// lane groups transpose them to word kg of step q = j.
+// lane groups transpose them to word kg of step j; four chunks' words are in
+// flight per wave, and one load brings four chunks' scales (a load each cost
+// 4 of 17 us at 2 tokens).  Bound by the latency of the weights: 4096 x 4096
+// takes 8.3 us at 32 tokens, one round of workgroups.
 constexpr int kWaves = 8;
+constexpr int kDeep = 4;  // chunks of weights in flight per wave
 
 // 8 codes of one 4-bit word as exact fp16, in column order (1024 + q and
 // 1024 + 16 q by bit operations, then one packed FMA).
@@ -109,9 +113,9 @@ __device__ inline void transpose_groups(uint32_t (&w)[4]) {
 }
 
 template <int BITS, int TT, int BT, bool VEC>
-__global__ __launch_bounds__(64 * kWaves, TT == 1 && BT * BITS <= 8 ? 4 : 2) void decode_mfma_kernel(
-    const _Float16* __restrict__ x, int64_t ldx, int m, const uint32_t* __restrict__ packed,
-    int64_t nw, int64_t rows, int64_t cols, const float* __restrict__ scales,
+__global__ __launch_bounds__(64 * kWaves, 2) void decode_mfma_kernel(
+    const _Float16* __restrict__ xp, int m, const uint32_t* __restrict__ packed, int64_t nw,
+    int64_t rows, int64_t cols, const float* __restrict__ scales,
     const float* __restrict__ zeros, int64_t ngroups, int groupsize, float* __restrict__ y,
     int64_t ldy, AdapterTile ad) {
   constexpr int WPC = 4 * BITS;          // words per chunk and row
@@ -122,6 +126,7 @@ __global__ __launch_bounds__(64 * kWaves, TT == 1 && BT * BITS <= 8 ? 4 : 2) voi
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, kg = lane >> 4;
   const int64_t r0 = (int64_t)blockIdx.x * 16 * BT;
   const int nch = (int)(cols / 128);
+  const int cb = nch * wave / kWaves, ce = nch * (wave + 1) / kWaves;  // this wave's chunks
   const uint32_t* wrow[BT];
   const float *srow[BT], *zrow[BT];
 #pragma unroll
@@ -131,16 +136,11 @@ __global__ __launch_bounds__(64 * kWaves, TT == 1 && BT * BITS <= 8 ? 4 : 2) voi
     srow[b] = scales + rr * ngroups;
     zrow[b] = zeros + rr * ngroups;
   }
-  const _Float16* xrow[TT];
-#pragma unroll
-  for (int t = 0; t < TT; ++t) xrow[t] = x + (int64_t)min(16 * t + n, m - 1) * ldx + 8 * kg;
-
-  uint32_t wv[2][BT][NW];
+  uint32_t wv[kDeep][BT][NW];
+  float sv[BT], zv[BT];  // lane group kg: the block's chunk kg
   half8 xv[2][TT][4];
-  float sv[2][BT], zv[2][BT];
-  auto fetch = [&](int slot, int c) {  // chunks past the end read the last one
+  auto fetch_w = [&](int slot, int c) {  // chunks past the end read the last one
     const int64_t cc = min(c, nch - 1);
-    const int64_t g = cc * 128 / groupsize;
 #pragma unroll
     for (int b = 0; b < BT; ++b) {
       if constexpr (BITS == 4) {
@@ -157,17 +157,29 @@ __global__ __launch_bounds__(64 * kWaves, TT == 1 && BT * BITS <= 8 ? 4 : 2) voi
           wv[slot][b][2 * q + 1] = v.y;
         }
       }
-      sv[slot][b] = srow[b][g];
-      zv[slot][b] = zrow[b][g];
     }
+  };
+  auto fetch_sz = [&](int c) {
+    const int64_t g = (int64_t)min(c + kg, nch - 1) * 128 / groupsize;
+#pragma unroll
+    for (int b = 0; b < BT; ++b) {
+      sv[b] = srow[b][g];
+      zv[b] = zrow[b][g];
+    }
+  };
+  auto fetch_x = [&](int slot, int c) {
+    const int64_t cc = min(c, nch - 1);
 #pragma unroll
     for (int t = 0; t < TT; ++t)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        xv[slot][t][q] = *reinterpret_cast<const half8*>(xrow[t] + 128 * cc + 32 * q);
+        xv[slot][t][q] = *reinterpret_cast<const half8*>(xp + ((t * nch + cc) * 4 + q) * 512 + 8 * lane);
   };
-  fetch(0, wave);
-  fetch(1, wave + kWaves);
+#pragma unroll
+  for (int i = 0; i < kDeep; ++i) fetch_w(i, cb + i);
+  fetch_sz(cb);
+  fetch_x(0, cb);
+  fetch_x(1, cb + 1);
   // this thread's outputs' low-rank part, its loads beside the first chunks'
   float low[PER];
 #pragma unroll
@@ -183,11 +195,18 @@ __global__ __launch_bounds__(64 * kWaves, TT == 1 && BT * BITS <= 8 ? 4 : 2) voi
   for (int t = 0; t < TT; ++t)
 #pragma unroll
     for (int b = 0; b < BT; ++b) acc[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int c0 = wave; c0 < nch; c0 += 2 * kWaves) {
+  for (int c0 = cb; c0 < ce; c0 += 4) {
+    float sc[BT], zc[BT];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = c0 + kWaves * i;
-      if (c < nch) {
+    for (int b = 0; b < BT; ++b) {
+      sc[b] = sv[b];
+      zc[b] = zv[b];
+    }
+    if (c0 + 4 < ce) fetch_sz(c0 + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + i;
+      if (c < ce) {
         f32x4 d[TT][BT], dx[TT];
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
@@ -197,33 +216,36 @@ __global__ __launch_bounds__(64 * kWaves, TT == 1 && BT * BITS <= 8 ? 4 : 2) voi
         }
         if constexpr (BITS == 4) {
 #pragma unroll
-          for (int b = 0; b < BT; ++b) transpose_groups(wv[i][b]);
+          for (int b = 0; b < BT; ++b) transpose_groups(wv[i % kDeep][b]);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
 #pragma unroll
           for (int t = 0; t < TT; ++t)
-            dx[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[i][t][q], ones, dx[t], 0, 0, 0);
+            dx[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[i & 1][t][q], ones, dx[t], 0, 0, 0);
 #pragma unroll
           for (int b = 0; b < BT; ++b) {
             half8 qv;
-            if constexpr (BITS == 4) qv = codes4(wv[i][b][q]);
-            else qv = codes8(wv[i][b][2 * q], wv[i][b][2 * q + 1]);
+            if constexpr (BITS == 4) qv = codes4(wv[i % kDeep][b][q]);
+            else qv = codes8(wv[i % kDeep][b][2 * q], wv[i % kDeep][b][2 * q + 1]);
 #pragma unroll
             for (int t = 0; t < TT; ++t)
-              d[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[i][t][q], qv, d[t][b], 0, 0, 0);
+              d[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[i & 1][t][q], qv, d[t][b], 0, 0, 0);
           }
         }
+        if (c + kDeep < ce) fetch_w(i % kDeep, c + kDeep);
+        if (c + 2 < ce) fetch_x(i & 1, c + 2);
 #pragma unroll
-        for (int b = 0; b < BT; ++b)
+        for (int b = 0; b < BT; ++b) {
+          const float s = __shfl(sc[b], n + 16 * i, 64), z = __shfl(zc[b], n + 16 * i, 64);
 #pragma unroll
           for (int t = 0; t < TT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              acc[t][b][e] = __builtin_fmaf(
-                  sv[i][b], __builtin_fmaf(-zv[i][b], dx[t][e], d[t][b][e]), acc[t][b][e]);
+              acc[t][b][e] =
+                  __builtin_fmaf(s, __builtin_fmaf(-z, dx[t][e], d[t][b][e]), acc[t][b][e]);
+        }
       }
-      if (c + 2 * kWaves < nch) fetch(i, c + 2 * kWaves);
     }
   }
 #pragma unroll
@@ -329,7 +351,7 @@ AdapterTile from_token(const AdapterTile& ad, int64_t t0) {
 }
 
 struct DecodeCall {
-  const _Float16* x;
+  const _Float16 *x, *xp;
   int64_t ldx, m;
   const uint32_t* packed;
   int64_t rows, cols;
@@ -346,7 +368,7 @@ void decode_mfma(const DecodeCall& c, const AdapterTile& ad, int64_t t0, int mt,
   const dim3 grid((unsigned)ceil_div(c.rows, 16 * BT));
 #define GPTQ_DECODE(V)                                                                           \
   hipLaunchKernelGGL((decode_mfma_kernel<BITS, TT, BT, V>), grid, dim3(64 * kWaves), 0, s,       \
-                     c.x + t0 * c.ldx, c.ldx, mt, c.packed, packed_words(c.cols, BITS), c.rows,  \
+                     c.xp + t0 * c.cols, mt, c.packed, packed_words(c.cols, BITS), c.rows,       \
                      c.cols, c.scales, c.zeros, ceil_div(c.cols, c.groupsize), c.groupsize,      \
                      c.y + t0 * c.ldy, c.ldy, from_token(ad, t0))
   if (vec) GPTQ_DECODE(true);
@@ -358,14 +380,19 @@ template <int BITS>
 hipError_t decode_mfma_passes(const DecodeCall& c, const AdapterTile& ad, hipStream_t s) {
   for (int64_t t0 = 0; t0 < c.m; t0 += 64) {
     const int mt = (int)(c.m - t0 < 64 ? c.m - t0 : 64);
-    // 32 outputs per workgroup halve x's traffic where rows give enough of them
-    const bool wide = c.rows >= 32 * 256;
+    // 16 outputs per workgroup, one workgroup per CU at a time: 8.3 us a round
+    // of 4096 outputs at 32 tokens; 48 outputs take 19 us a round of 12288
+    const bool wide = c.rows > 8192;
     if (mt <= 16) {
-      if (wide) decode_mfma<BITS, 1, 2>(c, ad, t0, mt, s);
+      if (wide) decode_mfma<BITS, 1, 3>(c, ad, t0, mt, s);
       else decode_mfma<BITS, 1, 1>(c, ad, t0, mt, s);
     } else if (mt <= 32) {
-      if (wide) decode_mfma<BITS, 2, 2>(c, ad, t0, mt, s);
-      else decode_mfma<BITS, 2, 1>(c, ad, t0, mt, s);
+      bool done = false;
+      if constexpr (BITS == 4) {  // 8 bits: the registers do not hold 48 outputs
+        if (wide) decode_mfma<BITS, 2, 3>(c, ad, t0, mt, s);
+        done = wide;
+      }
+      if (!done) decode_mfma<BITS, 2, 1>(c, ad, t0, mt, s);
     } else {
       decode_mfma<BITS, 4, 1>(c, ad, t0, mt, s);
     }
@@ -396,17 +423,23 @@ hipError_t decode_rows(const DecodeCall& c, const AdapterTile& ad, hipStream_t s
 
 }  // namespace
 
-hipError_t launch_decode_adapters(const _Float16* x, int64_t ldx, int64_t m,
+// two tokens or more, 4 or 8 bits, whole 128-column chunks inside groups,
+// 16-byte aligned rows
+bool decode_mfma_ok(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed, int bits,
+                    int64_t cols, int groupsize, const int* g_idx) {
+  return m >= 2 && (bits == 4 || bits == 8) && g_idx == nullptr && cols % 128 == 0 &&
+         (groupsize % 128 == 0 || groupsize >= cols) && ldx % 8 == 0 &&
+         (reinterpret_cast<uintptr_t>(x) & 15) == 0 &&
+         (reinterpret_cast<uintptr_t>(packed) & 15) == 0;
+}
+
+hipError_t launch_decode_adapters(const _Float16* x, const _Float16* xp, int64_t ldx, int64_t m,
                                   const uint32_t* packed, int bits, int64_t rows, int64_t cols,
                                   const float* scales, const float* zeros, int groupsize,
                                   const int* g_idx, const AdapterTile& ad, float* y, int64_t ldy,
                                   hipStream_t s) {
-  const DecodeCall c{x, ldx, m, packed, rows, cols, scales, zeros, groupsize, g_idx, y, ldy};
-  const bool words = g_idx == nullptr && (reinterpret_cast<uintptr_t>(packed) & 15) == 0;
-  // whole 128-column chunks inside groups, 16-byte aligned x rows
-  if (m >= 2 && (bits == 4 || bits == 8) && words && cols % 128 == 0 &&
-      (groupsize % 128 == 0 || groupsize >= cols) && ldx % 8 == 0 &&
-      (reinterpret_cast<uintptr_t>(x) & 15) == 0)
+  const DecodeCall c{x, xp, ldx, m, packed, rows, cols, scales, zeros, groupsize, g_idx, y, ldy};
+  if (decode_mfma_ok(x, ldx, m, packed, bits, cols, groupsize, g_idx))
     return bits == 4 ? decode_mfma_passes<4>(c, ad, s) : decode_mfma_passes<8>(c, ad, s);
   if (gemv_fast_ok(bits, cols, groupsize, g_idx, packed))
     return launch_gemv_adapters(x, ldx, m, packed, bits, rows, cols, scales, zeros, groupsize, ad, y,

@@ -34,8 +34,14 @@ struct Carve {
 
 int rank_pitch(int rank) { return (int)round_up(rank, 16); }
 
+// The pitch of a matrix of the workspace whose rows the fp16 product reads 64
+// bytes at a time: 256 bytes more than a multiple of 128, so the rows of a
+// tile start on different memory channels.
+int64_t gemm_pitch(int64_t k) { return k + 128; }
+
 struct BackwardLayout {
-  int64_t kp;  // rows padded to the fp16 product's K
+  int64_t kp;   // rows padded to the fp16 product's K
+  int64_t ldt;  // pitch of the transposed weights and of dy's copy
   size_t wt, dyp, v, dv, bt, list, chunks, ranges, part_a, part_b, total;
 };
 
@@ -43,8 +49,9 @@ BackwardLayout backward_layout(int64_t m, int64_t rows, int64_t cols, int64_t co
   BackwardLayout L{};
   Carve c;
   L.kp = round_up(rows, kKPad);
-  L.wt = c.take(cols * L.kp, 2);
-  L.dyp = c.take(L.kp == rows ? 0 : m * L.kp, 2);
+  L.ldt = gemm_pitch(L.kp);
+  L.wt = c.take(cols * L.ldt, 2);
+  L.dyp = c.take(L.kp == rows ? 0 : m * L.ldt, 2);
   if (count > 0) {
     const int64_t chunks = grad_chunks(m, count);
     L.v = c.take(m * rank_pitch(rank), 4);
@@ -78,8 +85,8 @@ HeadLayout head_layout(int64_t m, int64_t rows, int64_t cols) {
   L.pieces = ceil_div(rows, w);
   L.lse = c.take(m, 4);
   L.scale = c.take(m, 4);
-  L.probs = c.take(L.tokens * w, 2);
-  L.wt = c.take(cols * w, 2);
+  L.probs = c.take(L.tokens * gemm_pitch(w), 2);
+  L.wt = c.take(cols * gemm_pitch(w), 2);
   L.acc = c.take(L.pieces > 1 ? L.tokens * cols : 0, 4);
   L.total = c.at;
   return L;
@@ -90,14 +97,19 @@ size_t partials_bytes(int64_t m, int64_t rows) {
   return align_up((size_t)(head_tiles(8, m, rows) * m) * sizeof(float2));
 }
 
-// the tokens' v, and the split product's sums (8 bits: the smaller tiles may
-// split less)
+// The tokens' v, then what the product needs beside it: the splits' sums
+// (many tokens), or x in the decode product's order (whole 64-token passes).
+size_t forward_v_bytes(int64_t m, int rank) {
+  return align_up((size_t)m * rank_pitch(rank) * sizeof(float));
+}
+
 size_t forward_bytes(int64_t m, int64_t rows, int64_t cols, int rank) {
   // groups of 128: the most splits a layer of these sizes can have
   const int s4 = linear_splits(4, m, rows, cols, 128), s8 = linear_splits(8, m, rows, cols, 128);
   const int splits = s4 > s8 ? s4 : s8;
-  return align_up((size_t)m * rank_pitch(rank) * sizeof(float)) +
-         (splits > 1 ? align_up((size_t)splits * m * rows * sizeof(float)) : 0);
+  const size_t sums = splits > 1 ? (size_t)splits * m * rows * sizeof(float) : 0;
+  const size_t xp = cols % 128 == 0 ? (size_t)round_up(m, 64) * cols * sizeof(_Float16) : 0;
+  return forward_v_bytes(m, rank) + align_up(sums > xp ? sums : xp);
 }
 
 bool sizes_ok(int64_t m, int64_t rows, int64_t cols, int bits, int groupsize) {
@@ -165,7 +177,9 @@ AdapterTile forward_tile(const gptq_adapters* ad, int64_t rows, const float* v) 
 // the L2), so the limit falls with the rank.
 hipError_t shrink(const ShrinkJob& job, int64_t m, hipStream_t s) {
   if (m * job.ldv <= 8192) return launch_shrink_rows(job, m, s);
-  return launch_shrink_tiles(job, nullptr, m, s);
+  const hipError_t e = launch_shrink_tiles(job, nullptr, m, s);
+  if (e != hipSuccess || job.xp == nullptr) return e;
+  return launch_pack_x(job.x, job.ldx, m, job.K, job.xp, s);
 }
 
 #define GPTQ_TRY(call)                             \
@@ -210,9 +224,14 @@ gptq_status gptq_dequant_gemm_adapters(const void* x, int64_t m, int64_t cols, i
       gptq_adapters_workspace_bytes(GPTQ_OP_FORWARD_ADAPTERS, m, rows, cols, ad->count, ad->rank));
   if (ok != GPTQ_OK) return ok;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const _Float16* xh = reinterpret_cast<const _Float16*>(x);
   float* v = reinterpret_cast<float*>(workspace);
-  GPTQ_TRY(shrink(forward_job(ad, x, ldx, cols, v), m, s));
-  GPTQ_TRY(launch_decode_adapters(reinterpret_cast<const _Float16*>(x), ldx, m, packed, bits, rows,
+  ShrinkJob job = forward_job(ad, x, ldx, cols, v);
+  if (decode_mfma_ok(xh, ldx, m, packed, bits, cols, groupsize, g_idx))
+    job.xp = reinterpret_cast<_Float16*>(reinterpret_cast<char*>(workspace) +
+                                         forward_v_bytes(m, ad->rank));
+  GPTQ_TRY(shrink(job, m, s));
+  GPTQ_TRY(launch_decode_adapters(xh, job.xp, ldx, m, packed, bits, rows,
                                   cols, scales, zeros, groupsize, g_idx, forward_tile(ad, rows, v),
                                   y, ldy, s));
   return GPTQ_OK;
@@ -241,7 +260,8 @@ gptq_status gptq_linear_forward_adapters(const void* x, int64_t m, int64_t cols,
   GPTQ_TRY(launch_linear_forward_adapters(bits, reinterpret_cast<const _Float16*>(x), ldx, m,
                                           packed, rows, cols, scales, zeros, groupsize, relu == 1,
                                           forward_tile(ad, rows, v),
-                                          v + align_up(m * rank_pitch(ad->rank) * 4) / 4,
+                                          reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) +
+                                                                   forward_v_bytes(m, ad->rank)),
                                           reinterpret_cast<_Float16*>(y), ldy, s));
   return GPTQ_OK;
 }
@@ -281,12 +301,12 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
   int64_t ldg = lddy;
   if (L.kp != rows) {
     _Float16* p = reinterpret_cast<_Float16*>(ws + L.dyp);
-    GPTQ_TRY(launch_pad_rows(g, lddy, m, rows, L.kp, p, s));
+    GPTQ_TRY(launch_pad_rows(g, lddy, m, rows, L.kp, L.ldt, p, s));
     g = p;
-    ldg = L.kp;
+    ldg = L.ldt;
   }
   GPTQ_TRY(launch_dequant_transposed(packed, bits, rows, cols, scales, zeros, groupsize, g_idx, L.kp,
-                                     wt, s));
+                                     L.ldt, wt, s));
   AdapterTile tile{};
   if (ad != nullptr) {
     float* v = reinterpret_cast<float*>(ws + L.v);
@@ -333,7 +353,7 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
     tile.js = cols;
     tile.ns = 1;
   }
-  GPTQ_TRY(launch_gemm_nt_f16(g, ldg, m, wt, L.kp, cols, L.kp, ad != nullptr ? &tile : nullptr,
+  GPTQ_TRY(launch_gemm_nt_f16(g, ldg, m, wt, L.ldt, cols, L.kp, ad != nullptr ? &tile : nullptr,
                               reinterpret_cast<_Float16*>(dx), lddx, s));
   return GPTQ_OK;
 }
@@ -434,14 +454,14 @@ gptq_status head_backward(const void* h, int64_t m, int64_t cols, int64_t ldh,
     if (tt.logits != nullptr) tt.logits += t0 * top;
     for (int64_t v0 = 0; v0 < rows; v0 += L.width) {
       const int64_t w = rows - v0 < L.width ? rows - v0 : L.width;
-      const int64_t wp = round_up(w, kKPad);
+      const int64_t wp = round_up(w, kKPad), ld = gemm_pitch(wp);
       const bool last = v0 + w == rows;
       GPTQ_TRY(launch_head_probs(bits, x, ldh, mt, packed + v0 * nw, w, cols, scales + v0 * ng,
-                                 zeros + v0 * ng, groupsize, tg.inv_t, lse_eff + t0, P, wp, s));
-      GPTQ_TRY(launch_head_scatter(tt, mt, rows, v0, w, zk + t0 * top, lse + t0, P, wp, s));
+                                 zeros + v0 * ng, groupsize, tg.inv_t, lse_eff + t0, P, ld, s));
+      GPTQ_TRY(launch_head_scatter(tt, mt, rows, v0, w, zk + t0 * top, lse + t0, P, ld, s));
       GPTQ_TRY(launch_dequant_transposed(packed + v0 * nw, bits, w, cols, scales + v0 * ng,
-                                         zeros + v0 * ng, groupsize, nullptr, wp, wt, s));
-      GPTQ_TRY(launch_gemm_nt_acc(P, wp, mt, wt, wp, cols, wp, v0 == 0, acc, gscale + t0,
+                                         zeros + v0 * ng, groupsize, nullptr, wp, ld, wt, s));
+      GPTQ_TRY(launch_gemm_nt_acc(P, ld, mt, wt, ld, cols, wp, v0 == 0, acc, gscale + t0,
                                   last ? out : nullptr, lddh, s));
     }
   }
