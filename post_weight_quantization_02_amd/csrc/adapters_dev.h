@@ -31,35 +31,28 @@ template <int AT, int BT>
 __device__ inline void add_adapters(f32x4 (&acc)[AT][BT], const AdapterTile& ad, int64_t t0,
                                     int64_t m, int64_t n0, int64_t n) {
   const int lane = threadIdx.x & 63, li = lane & 15, kg = lane >> 4;
-  int id[AT][4];
+  int id[AT];  // of token 16 a + li
 #pragma unroll
-  for (int a = 0; a < AT; ++a)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t t = t0 + 16 * a + 4 * kg + i;
-      const int d = t < m ? ad.index[t] : -1;
-      id[a][i] = (d >= 0 && d < ad.count) ? d : -1;
-    }
+  for (int a = 0; a < AT; ++a) {
+    const int64_t t = t0 + 16 * a + li;
+    const int d = t < m ? ad.index[t] : -1;
+    id[a] = (d >= 0 && d < ad.count) ? d : -1;
+  }
   const int steps = (ad.rank + 3) / 4;
   int cur = -1;
   while (true) {
     int next = 0x7fffffff;
 #pragma unroll
     for (int a = 0; a < AT; ++a)
+      if (id[a] > cur && id[a] < next) next = id[a];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (id[a][i] > cur && id[a][i] < next) next = id[a][i];
-    next = min(next, __shfl_xor(next, 16, 64));
-    next = min(next, __shfl_xor(next, 32, 64));
+    for (int o = 8; o > 0; o >>= 1) next = min(next, __shfl_xor(next, o, 64));
     cur = __builtin_amdgcn_readfirstlane(next);
     if (cur == 0x7fffffff) break;  // every wave ends: cur grows each turn
     const _Float16* up = ad.up + cur * ad.stride;
 #pragma unroll
     for (int a = 0; a < AT; ++a) {
-      bool any = false;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) any |= id[a][i] == cur;
-      if (__ballot(any) == 0) continue;
+      if (__ballot(id[a] == cur) == 0) continue;
       const float* vrow = ad.v + min(t0 + 16 * a + li, m - 1) * ad.ldv + kg;
       f32x4 part[BT];
 #pragma unroll
@@ -75,10 +68,12 @@ __device__ inline void add_adapters(f32x4 (&acc)[AT][BT], const AdapterTile& ad,
         }
       }
 #pragma unroll
-      for (int b = 0; b < BT; ++b)
+      for (int i = 0; i < 4; ++i) {
+        const bool mine = __shfl(id[a], 4 * kg + i, 64) == cur;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (id[a][i] == cur) acc[a][b][i] += part[b][i];
+        for (int b = 0; b < BT; ++b)
+          if (mine) acc[a][b][i] += part[b][i];
+      }
     }
   }
 }

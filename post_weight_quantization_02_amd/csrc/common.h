@@ -194,11 +194,15 @@ hipError_t launch_pad_rows(const _Float16* src, int64_t lds, int64_t m, int64_t 
 // C = A B^T, A m x K, B n x K (K % kKPad == 0, 16-byte aligned rows)
 hipError_t launch_gemm_nt_f16(const _Float16* A, int64_t lda, int64_t m, const _Float16* B,
                               int64_t ldb, int64_t n, int64_t K, const AdapterTile* ad,
-                              _Float16* C, int64_t ldc, hipStream_t s);
+                              float* sums, _Float16* C, int64_t ldc, hipStream_t s);
 // C32 (+)= A B^T, or with C16 the finished rows: C16 = fp16(scale[t] (C32 + A B^T))
 hipError_t launch_gemm_nt_acc(const _Float16* A, int64_t lda, int64_t m, const _Float16* B,
                               int64_t ldb, int64_t n, int64_t K, bool first, float* C32,
-                              const float* scale, _Float16* C16, int64_t ldc, hipStream_t s);
+                              const float* scale, float* sums, _Float16* C16, int64_t ldc,
+                              hipStream_t s);
+// splits of K when the tiles leave CUs idle (1: none); their fp32 sums,
+// splits x m x n, go to the workspace
+int gemm_splits(int64_t m, int64_t n, int64_t K);
 // the vocabulary losses
 // what is learnt: K entries per token, logits (their softmax) or one label
 struct HeadTargets {

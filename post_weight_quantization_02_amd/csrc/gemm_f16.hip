@@ -7,6 +7,7 @@
 // (at most 2^-11 of its size, 2^-25 below 2^-14); the products are exact in
 // fp32 and summed there.
 #include "adapters_dev.h"
+#include "tile_grid.h"
 
 namespace gptq {
 namespace {
@@ -101,14 +102,22 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const _Float16* __restric
 }
 
 // ------------------------------------------------------------ C = A B^T
-// (32 AT) x (32 BT) outputs per workgroup of four waves, each a quadrant of
-// AT x BT tiles of v_mfma_f32_16x16x32_f16.  32 columns of K of both operands
-// go straight into a 4-stage LDS ring by global_load_lds_dwordx4; a row of a
-// stage is 64 bytes, its four 16-byte pieces permuted by (row >> 2) & 3 so
-// the 16 rows a fragment read touches use 16 distinct bank groups.  Rows past
-// the operands are read clamped and not stored.
-constexpr int KC = 32;
-constexpr int NST = 4;
+// 32 AT tokens x 64 BT outputs per workgroup of eight waves (two by four),
+// each AT x BT tiles of v_mfma_f32_16x16x32_f16.  64 columns of K of both
+// operands go straight into a stage of LDS by global_load_lds_dwordx4; a row
+// of a stage is 128 bytes, its eight 16-byte pieces permuted by (row >> 1) & 7
+// so the 16 rows that a fragment read touches use 16 distinct bank groups.
+// Rows past the operands are read clamped and not stored.
+//
+// Measured at 8192 x 4096 outputs, K = 11008 (8192: 4096 x 4096 outputs):
+// 256 x 256 with two stages of 64 columns 1213 TF/s (1273); four stages of 32
+// columns 1146 (1158); four waves of 128 x 128 1026 (1119); 128 x 256 1068
+// (1096); with both pitches a multiple of 2 KB 256 x 256 falls to 1065 (1263).
+// The library's fp16 product reaches 1060-1090.  Bound by the matrix units'
+// clock under load and the wait at each stage.  128 x 128 with three stages is
+// the shape where 256 x 256 leaves CUs idle (1000 x 4096, K = 8192: 85 us
+// against 105 with four waves and 32 columns).
+constexpr int KC = 64;
 
 typedef __attribute__((address_space(3))) void lds_void;
 
@@ -124,56 +133,68 @@ __device__ inline void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// What becomes of the sums: fp16 (with adapters first, or scaled row by row on
+// top of c32: the last of several products), fp32 on top of c32 (the others),
+// or the fp32 sums of one split of K.
+enum GemmMode { kStore = 0, kStoreAdapters = 1, kAccumulate = 2, kFinish = 3, kSplit = 4 };
+
 struct GemmOut {
-  AdapterTile ad;        // kStore with adapters
+  AdapterTile ad;
   _Float16* c16;
   int64_t ldc;
-  float* c32;            // m x n
-  const float* scale;
-  bool first;
+  float* c32;          // m x n
+  const float* scale;  // m
+  bool first;          // c32 holds nothing yet
+  float* sums;         // splits x m x n
 };
 
-enum GemmMode { kStore = 0, kStoreAdapters = 1, kAccumulate = 2, kFinish = 3 };
-
-template <int AT, int BT, int MODE>
-__global__ __launch_bounds__(256, 1) void gemm_nt_kernel(const _Float16* __restrict__ A,
+template <int AT, int BT, int NST, int MODE>
+__global__ __launch_bounds__(512, 1) void gemm_nt_kernel(const _Float16* __restrict__ A,
                                                          int64_t lda, int64_t m,
                                                          const _Float16* __restrict__ B,
                                                          int64_t ldb, int64_t n, int64_t K,
-                                                         int64_t ntn, GemmOut o) {
-  constexpr int TM = 32 * AT, TN = 32 * BT;
+                                                         TileGrid grid, GemmOut o) {
+  constexpr int TM = 32 * AT, TN = 64 * BT;
   constexpr int ABYTES = TM * KC * 2, STAGE = (TM + TN) * KC * 2;
-  constexpr int AU = TM / 64, BU = TN / 64;  // 16-row loads per wave and stage
-  constexpr int LPS = AU + BU;
+  constexpr int AU = TM / 64, BU = TN / 64, LPS = AU + BU;  // 8-row loads per wave and stage
   __shared__ __attribute__((aligned(1024))) char ring[NST * STAGE];
-  const int64_t tm = blockIdx.x / ntn, tn = blockIdx.x % ntn;
+  int64_t tm, tn;
+  if (!tile_of(grid, blockIdx.x, tm, tn)) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1, li = lane & 15, kg = lane >> 4;
+  const int wm = wave >> 2, wn = wave & 3, li = lane & 15, kg = lane >> 4;
   const int64_t t0 = tm * TM, n0 = tn * TN;
+  const int all = (int)(K / KC);
+  const int kb = MODE == kSplit ? (int)((int64_t)all * blockIdx.y / gridDim.y) : 0;
+  const int ke = MODE == kSplit ? (int)((int64_t)all * (blockIdx.y + 1) / gridDim.y) : all;
 
-  const _Float16* asrc[AU];
-  const _Float16* bsrc[BU];
+  // this lane's 16 bytes of each load, from the tile's first row (64-bit: a
+  // row pitch may be any user's)
+  const char* asrc[AU];
+  const char* bsrc[BU];
 #pragma unroll
   for (int u = 0; u < AU; ++u) {
-    const int row = 16 * (wave + 4 * u) + (lane >> 2);
-    asrc[u] = A + min(t0 + row, m - 1) * lda + 8 * ((lane & 3) ^ ((row >> 2) & 3));
+    const int row = 8 * (wave + 8 * u) + (lane >> 3);
+    asrc[u] = reinterpret_cast<const char*>(A + min(t0 + row, m - 1) * lda) +
+              16 * ((lane & 7) ^ ((row >> 1) & 7));
   }
 #pragma unroll
   for (int u = 0; u < BU; ++u) {
-    const int row = 16 * (wave + 4 * u) + (lane >> 2);
-    bsrc[u] = B + min(n0 + row, n - 1) * ldb + 8 * ((lane & 3) ^ ((row >> 2) & 3));
+    const int row = 8 * (wave + 8 * u) + (lane >> 3);
+    bsrc[u] = reinterpret_cast<const char*>(B + min(n0 + row, n - 1) * ldb) +
+              16 * ((lane & 7) ^ ((row >> 1) & 7));
   }
-  auto issue = [&](int64_t k) {
-    char* st = ring + (int)(k % NST) * STAGE;
+  auto issue = [&](int k) {
+    char* st = ring + ((k - kb) % NST) * STAGE;
+    const uint32_t off = (uint32_t)k * (KC * 2);
 #pragma unroll
     for (int u = 0; u < AU; ++u)
-      __builtin_amdgcn_global_load_lds((const void*)(asrc[u] + k * KC),
-                                       (lds_void*)(st + 1024 * (wave + 4 * u)), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((const void*)(asrc[u] + off),
+                                       (lds_void*)(st + 1024 * (wave + 8 * u)), 16, 0, 0);
 #pragma unroll
     for (int u = 0; u < BU; ++u)
-      __builtin_amdgcn_global_load_lds((const void*)(bsrc[u] + k * KC),
-                                       (lds_void*)(st + ABYTES + 1024 * (wave + 4 * u)), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((const void*)(bsrc[u] + off),
+                                       (lds_void*)(st + ABYTES + 1024 * (wave + 8 * u)), 16, 0, 0);
   };
   f32x4 acc[AT][BT];
 #pragma unroll
@@ -181,26 +202,30 @@ __global__ __launch_bounds__(256, 1) void gemm_nt_kernel(const _Float16* __restr
 #pragma unroll
     for (int b = 0; b < BT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int64_t nk = K / KC;
-  for (int64_t k = 0; k < NST - 1 && k < nk; ++k) issue(k);
-  const int frag = 64 * li + 16 * (kg ^ ((li >> 2) & 3));
-  for (int64_t k = 0; k < nk; ++k) {
-    if (k + 2 < nk) wait_vm<2 * LPS>();
-    else if (k + 1 < nk) wait_vm<LPS>();
+  for (int k = kb; k < kb + NST - 1 && k < ke; ++k) issue(k);
+  for (int k = kb; k < ke; ++k) {
+    // stage k has landed for this wave, the later ones may be in flight; the
+    // barrier publishes it, and behind it nobody reads the stage before
+    if (NST == 3 && k + 1 < ke) wait_vm<LPS>();
     else wait_vm<0>();
     lds_barrier();
-    if (k + NST - 1 < nk) issue(k + NST - 1);
-    const char* as = ring + (int)(k % NST) * STAGE + wm * 16 * AT * 64 + frag;
-    const char* bs = ring + (int)(k % NST) * STAGE + ABYTES + wn * 16 * BT * 64 + frag;
-    half8 bf[BT];
+    if (k + NST - 1 < ke) issue(k + NST - 1);
+    const char* st = ring + ((k - kb) % NST) * STAGE;
 #pragma unroll
-    for (int b = 0; b < BT; ++b) bf[b] = *reinterpret_cast<const half8*>(bs + 1024 * b);
+    for (int s = 0; s < KC / 32; ++s) {
+      const int frag = 2 * KC * li + 16 * ((4 * s + kg) ^ ((li >> 1) & 7));
+      const char* as = st + wm * (16 * AT * 2 * KC) + frag;
+      const char* bs = st + ABYTES + wn * (16 * BT * 2 * KC) + frag;
+      half8 bf[BT];
 #pragma unroll
-    for (int a = 0; a < AT; ++a) {
-      const half8 af = *reinterpret_cast<const half8*>(as + 1024 * a);
+      for (int b = 0; b < BT; ++b) bf[b] = *reinterpret_cast<const half8*>(bs + 32 * KC * b);
 #pragma unroll
-      for (int b = 0; b < BT; ++b)
-        acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(af, bf[b], acc[a][b], 0, 0, 0);
+      for (int a = 0; a < AT; ++a) {
+        const half8 af = *reinterpret_cast<const half8*>(as + 32 * KC * a);
+#pragma unroll
+        for (int b = 0; b < BT; ++b)
+          acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(af, bf[b], acc[a][b], 0, 0, 0);
+      }
     }
   }
 
@@ -218,6 +243,10 @@ __global__ __launch_bounds__(256, 1) void gemm_nt_kernel(const _Float16* __restr
         const int64_t c = nw + 16 * b + li;
         if (c >= n) continue;
         float v = acc[a][b][i];
+        if constexpr (MODE == kSplit) {
+          o.sums[((int64_t)blockIdx.y * m + t) * n + c] = v;
+          continue;
+        }
         if constexpr (MODE == kAccumulate || MODE == kFinish)
           if (!o.first) v += o.c32[t * n + c];
         if constexpr (MODE == kAccumulate) o.c32[t * n + c] = v;
@@ -226,23 +255,82 @@ __global__ __launch_bounds__(256, 1) void gemm_nt_kernel(const _Float16* __restr
     }
 }
 
+// The splits added in order, then as the modes above.
+template <int MODE>
+__global__ __launch_bounds__(256) void gemm_reduce_kernel(int splits, int64_t m, int64_t n,
+                                                          GemmOut o) {
+  const int64_t t = blockIdx.x, c = (int64_t)blockIdx.y * 256 + threadIdx.x;
+  if (c >= n) return;
+  float v = 0.f;
+#pragma unroll 8
+  for (int k = 0; k < splits; ++k) v += o.sums[(k * m + t) * n + c];
+  if constexpr (MODE == kStoreAdapters) {
+    const int a = o.ad.index[t];
+    if (a >= 0 && a < o.ad.count) {
+      const _Float16* up = o.ad.up + a * o.ad.stride + c * o.ad.ns;
+      float low = 0.f;
+#pragma unroll 8
+      for (int j = 0; j < o.ad.rank; ++j)
+        low = __builtin_fmaf(o.ad.v[t * o.ad.ldv + j], (float)up[j * o.ad.js], low);
+      v += low;
+    }
+  }
+  if constexpr (MODE == kAccumulate || MODE == kFinish)
+    if (!o.first) v += o.c32[t * n + c];
+  if constexpr (MODE == kAccumulate) o.c32[t * n + c] = v;
+  else o.c16[t * o.ldc + c] = (_Float16)(MODE == kFinish ? o.scale[t] * v : v);
+}
+
+// A block of tiles per XCD that is as near a square as 1, 2, 4 or 8 XCDs along
+// the tokens make it.
+TileGrid gemm_grid(int64_t ntm, int64_t ntn) {
+  TileGrid g{ntm, ntn, kXcds, 1};
+  while (g.xm > 1 && ceil_div(ntm, g.xm) < ceil_div(ntn, kXcds / g.xm)) g.xm /= 2;
+  const int64_t mine = ceil_div(ntm, g.xm);
+  g.gm = mine < 8 ? (int)mine : 8;
+  return g;
+}
+
+// A round of 256 large tiles takes 2.5 times one of small tiles.
+bool large_tiles(int64_t m, int64_t n) {
+  const int64_t large = ceil_div(ceil_div(m, 256) * ceil_div(n, 256), 256);
+  const int64_t small = ceil_div(ceil_div(m, 128) * ceil_div(n, 128), 256);
+  return 5 * large <= 2 * small;
+}
+
 template <int MODE>
 hipError_t launch_gemm(const _Float16* A, int64_t lda, int64_t m, const _Float16* B, int64_t ldb,
                        int64_t n, int64_t K, const GemmOut& o, hipStream_t s) {
-  // 256 x 256 tiles when they fill the CUs, else 128 x 128
-  if (ceil_div(m, 256) * ceil_div(n, 256) >= 192) {
-    const int64_t ntn = ceil_div(n, 256);
-    hipLaunchKernelGGL((gemm_nt_kernel<8, 8, MODE>), dim3((unsigned)(ceil_div(m, 256) * ntn)),
-                       dim3(256), 0, s, A, lda, m, B, ldb, n, K, ntn, o);
+  const int splits = gemm_splits(m, n, K);
+  if (splits > 1) {
+    const TileGrid g = gemm_grid(ceil_div(m, 128), ceil_div(n, 128));
+    hipLaunchKernelGGL((gemm_nt_kernel<4, 2, 3, kSplit>),
+                       dim3((unsigned)g.blocks(), (unsigned)splits), dim3(512), 0, s, A, lda, m, B,
+                       ldb, n, K, g, o);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(gemm_reduce_kernel<MODE>, dim3((unsigned)m, (unsigned)ceil_div(n, 256)),
+                       dim3(256), 0, s, splits, m, n, o);
+  } else if (large_tiles(m, n)) {
+    const TileGrid g = gemm_grid(ceil_div(m, 256), ceil_div(n, 256));
+    hipLaunchKernelGGL((gemm_nt_kernel<8, 4, 2, MODE>), dim3((unsigned)g.blocks()), dim3(512), 0, s,
+                       A, lda, m, B, ldb, n, K, g, o);
   } else {
-    const int64_t ntn = ceil_div(n, 128);
-    hipLaunchKernelGGL((gemm_nt_kernel<4, 4, MODE>), dim3((unsigned)(ceil_div(m, 128) * ntn)),
-                       dim3(256), 0, s, A, lda, m, B, ldb, n, K, ntn, o);
+    const TileGrid g = gemm_grid(ceil_div(m, 128), ceil_div(n, 128));
+    hipLaunchKernelGGL((gemm_nt_kernel<4, 2, 3, MODE>), dim3((unsigned)g.blocks()), dim3(512), 0, s,
+                       A, lda, m, B, ldb, n, K, g, o);
   }
   return hipGetLastError();
 }
 
 }  // namespace
+
+int gemm_splits(int64_t m, int64_t n, int64_t K) {
+  const int64_t tiles = ceil_div(m, 128) * ceil_div(n, 128);
+  int64_t s = 256 / tiles;
+  if (s > K / KC / 4) s = K / KC / 4;
+  return s < 2 ? 1 : (int)s;
+}
 
 hipError_t launch_dequant_transposed(const uint32_t* packed, int bits, int64_t rows, int64_t cols,
                                      const float* scales, const float* zeros, int groupsize,
@@ -272,8 +360,9 @@ hipError_t launch_pad_rows(const _Float16* src, int64_t lds, int64_t m, int64_t 
 
 hipError_t launch_gemm_nt_f16(const _Float16* A, int64_t lda, int64_t m, const _Float16* B,
                               int64_t ldb, int64_t n, int64_t K, const AdapterTile* ad,
-                              _Float16* C, int64_t ldc, hipStream_t s) {
+                              float* sums, _Float16* C, int64_t ldc, hipStream_t s) {
   GemmOut o{};
+  o.sums = sums;
   o.c16 = C;
   o.ldc = ldc;
   if (ad == nullptr) return launch_gemm<kStore>(A, lda, m, B, ldb, n, K, o, s);
@@ -283,8 +372,10 @@ hipError_t launch_gemm_nt_f16(const _Float16* A, int64_t lda, int64_t m, const _
 
 hipError_t launch_gemm_nt_acc(const _Float16* A, int64_t lda, int64_t m, const _Float16* B,
                               int64_t ldb, int64_t n, int64_t K, bool first, float* C32,
-                              const float* scale, _Float16* C16, int64_t ldc, hipStream_t s) {
+                              const float* scale, float* sums, _Float16* C16, int64_t ldc,
+                              hipStream_t s) {
   GemmOut o{};
+  o.sums = sums;
   o.c16 = C16;
   o.ldc = ldc;
   o.c32 = C32;

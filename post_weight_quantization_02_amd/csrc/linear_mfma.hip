@@ -36,13 +36,13 @@
 //   * XCD-aware order: an XCD works on groups of 4 token tiles x all output
 //     tiles, 4 x 8 tiles at a time, so its L2 serves both operands.
 #include "adapters_dev.h"
+#include "tile_grid.h"
 
 namespace gptq {
 namespace {
 
 constexpr int KG = 128;    // input columns per stage
 constexpr int NSTAGE = 3;
-constexpr int kXcds = 8;
 constexpr int kGroupM = 4;  // token tiles per XCD-local group
 
 // What depends on the code width: a wave's outputs (WTN), the packed bytes of
@@ -453,19 +453,6 @@ __device__ inline void tile_targets(const f32x4 (&acc)[L::AT][L::BT], const Tail
   }
 }
 
-// The grid of one product: which tiles an XCD works on, and in which order.
-// Workgroup b runs on XCD b % 8.  The XCDs form an xm x (8 / xm) grid over the
-// token and output tiles; an XCD walks its token tiles in groups of gm, and
-// within a group output tile by output tile, so the ~32 workgroups it runs
-// at once share 4 x tiles and 8 weight tiles in its L2 (32 KB and 16 KB per
-// stage: the split that minimises its misses).  With fewer than 32 token
-// tiles xm falls below 8 so that an XCD still has 4 of them and the weights
-// are read by 8 / xm fewer XCDs.
-struct TileGrid {
-  int64_t ntm, ntn;
-  int xm, gm;
-};
-
 // The weights of one chunk are 64 (128) bytes of every packed row: rows whose
 // pitch is a multiple of 2 KB put them on an eighth of the memory channels,
 // and workgroups that run in step read them all at once.  Where an XCD has
@@ -488,15 +475,9 @@ __global__ __launch_bounds__(64 * W, 1) void linear_kernel(
   __shared__ __attribute__((aligned(1024))) char st1[L::STAGE];
   __shared__ __attribute__((aligned(1024))) char st2[L::STAGE];
 
-  const int64_t bid = blockIdx.x;
-  const int xcd = (int)(bid % kXcds);
-  const int64_t local = bid / kXcds;
-  const int xi = xcd % grid.xm, xj = xcd / grid.xm, xn = kXcds / grid.xm;
-  const int64_t ntj = (grid.ntn + xn - 1) / xn;
-  const int64_t grp = local / (grid.gm * ntj), idx = local % (grid.gm * ntj);
-  const int64_t tm = (grp * grid.gm + idx % grid.gm) * grid.xm + xi;
-  const int64_t tn = (idx / grid.gm) * xn + xj;
-  if (tm >= grid.ntm || tn >= grid.ntn) return;
+  int64_t tm, tn;
+  if (!tile_of(grid, blockIdx.x, tm, tn)) return;
+  const int xcd = (int)(blockIdx.x % kXcds);
   const int64_t t0 = tm * L::TM, n0 = tn * L::TN;
 
   const int tid = threadIdx.x;
@@ -620,6 +601,10 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restr
   y[t * ldy + r] = (_Float16)v;
 }
 
+// An XCD takes 4 token tiles x 8 output tiles at once (32 KB and 16 KB per
+// stage: the split that minimises its misses).  With fewer than 32 token
+// tiles xm falls below 8, so that an XCD still has 4 of them and the weights
+// are read by fewer XCDs.
 template <class L>
 TileGrid tile_grid(int64_t m, int64_t rows, bool store) {
   TileGrid g;
@@ -633,14 +618,10 @@ TileGrid tile_grid(int64_t m, int64_t rows, bool store) {
   return g;
 }
 
-int64_t grid_blocks(const TileGrid& g) {
-  // every XCD gets the same whole number of gm-token-tile groups
-  return kXcds * round_up(ceil_div(g.ntm, g.xm), g.gm) * ceil_div(g.ntn, kXcds / g.xm);
-}
-
 int64_t linear_blocks(int bits, int64_t m, int64_t rows) {
-  return grid_blocks(bits == 4 ? tile_grid<Lay<4, 8, 8>>(m, rows, true)
-                               : tile_grid<Lay<8, 8, 8>>(m, rows, true));
+  return (bits == 4 ? tile_grid<Lay<4, 8, 8>>(m, rows, true)
+                    : tile_grid<Lay<8, 8, 8>>(m, rows, true))
+      .blocks();
 }
 
 struct LinearCall {
@@ -662,7 +643,7 @@ hipError_t launch_tile(const LinearCall& c, const Tail& tail, int splits, hipStr
   const int64_t nw = c.cols * BITS / 32;
   const TileGrid grid = tile_grid<Lay<BITS, A, W>>(c.m, c.rows, TAIL == kStore);
   hipLaunchKernelGGL((linear_kernel<BITS, RELU, TAIL, A, W>),
-                     dim3((unsigned)grid_blocks(grid), (unsigned)splits), dim3(64 * W), 0, s, c.x,
+                     dim3((unsigned)grid.blocks(), (unsigned)splits), dim3(64 * W), 0, s, c.x,
                      c.ldx, c.m, c.packed, nw, c.rows, c.cols, c.scales, c.zeros, ngroups, gk, grid,
                      c.y, c.ldy, tail);
   return hipGetLastError();

@@ -34,6 +34,12 @@ struct Carve {
 
 int rank_pitch(int rank) { return (int)round_up(rank, 16); }
 
+// the sums of a split product
+int64_t split_sums(int64_t m, int64_t n, int64_t K) {
+  const int splits = gemm_splits(m, n, K);
+  return splits > 1 ? splits * m * n : 0;
+}
+
 // The pitch of a matrix of the workspace whose rows the fp16 product reads 64
 // bytes at a time: 256 bytes more than a multiple of 128, so the rows of a
 // tile start on different memory channels.
@@ -42,7 +48,7 @@ int64_t gemm_pitch(int64_t k) { return k + 128; }
 struct BackwardLayout {
   int64_t kp;   // rows padded to the fp16 product's K
   int64_t ldt;  // pitch of the transposed weights and of dy's copy
-  size_t wt, dyp, v, dv, bt, list, chunks, ranges, part_a, part_b, total;
+  size_t wt, dyp, sums, v, dv, bt, list, chunks, ranges, part_a, part_b, total;
 };
 
 BackwardLayout backward_layout(int64_t m, int64_t rows, int64_t cols, int64_t count, int rank) {
@@ -52,6 +58,7 @@ BackwardLayout backward_layout(int64_t m, int64_t rows, int64_t cols, int64_t co
   L.ldt = gemm_pitch(L.kp);
   L.wt = c.take(cols * L.ldt, 2);
   L.dyp = c.take(L.kp == rows ? 0 : m * L.ldt, 2);
+  L.sums = c.take(split_sums(m, cols, L.kp), 4);
   if (count > 0) {
     const int64_t chunks = grad_chunks(m, count);
     L.v = c.take(m * rank_pitch(rank), 4);
@@ -69,7 +76,7 @@ BackwardLayout backward_layout(int64_t m, int64_t rows, int64_t cols, int64_t co
 
 struct HeadLayout {
   int64_t tokens, width, pieces;  // tokens and vocabulary entries per pass, passes over the latter
-  size_t lse, scale, probs, wt, acc, total;
+  size_t lse, scale, probs, wt, acc, sums, total;
 };
 
 // A pass keeps at most 2^25 probabilities (64 MB, which the 256 MB Infinity
@@ -88,6 +95,11 @@ HeadLayout head_layout(int64_t m, int64_t rows, int64_t cols) {
   L.probs = c.take(L.tokens * gemm_pitch(w), 2);
   L.wt = c.take(cols * gemm_pitch(w), 2);
   L.acc = c.take(L.pieces > 1 ? L.tokens * cols : 0, 4);
+  // the last pass over the tokens may split more than the others
+  const int64_t rest = m % L.tokens;
+  const int64_t most = split_sums(L.tokens, cols, w);
+  const int64_t last = rest > 0 ? split_sums(rest, cols, w) : 0;
+  L.sums = c.take(most > last ? most : last, 4);
   L.total = c.at;
   return L;
 }
@@ -354,6 +366,7 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
     tile.ns = 1;
   }
   GPTQ_TRY(launch_gemm_nt_f16(g, ldg, m, wt, L.ldt, cols, L.kp, ad != nullptr ? &tile : nullptr,
+                              reinterpret_cast<float*>(ws + L.sums),
                               reinterpret_cast<_Float16*>(dx), lddx, s));
   return GPTQ_OK;
 }
@@ -462,7 +475,8 @@ gptq_status head_backward(const void* h, int64_t m, int64_t cols, int64_t ldh,
       GPTQ_TRY(launch_dequant_transposed(packed + v0 * nw, bits, w, cols, scales + v0 * ng,
                                          zeros + v0 * ng, groupsize, nullptr, wp, ld, wt, s));
       GPTQ_TRY(launch_gemm_nt_acc(P, ld, mt, wt, ld, cols, wp, v0 == 0, acc, gscale + t0,
-                                  last ? out : nullptr, lddh, s));
+                                  reinterpret_cast<float*>(ws + L.sums), last ? out : nullptr, lddh,
+                                  s));
     }
   }
   return GPTQ_OK;
