@@ -43,8 +43,9 @@ __global__ __launch_bounds__(256) void pack_x_kernel(const _Float16* __restrict_
 // v[t][j] for one token and four j per workgroup: a few tokens, each with an
 // adapter of its own (decode).  Bound by the read of the adapters' rows.
 template <bool VEC>
-__global__ __launch_bounds__(256) void shrink_rows_kernel(ShrinkJob job, int64_t m) {
+__global__ __launch_bounds__(256) void shrink_rows_kernel(ShrinkJob first, ShrinkJob second) {
   __shared__ float red[4][4];
+  const ShrinkJob& job = blockIdx.z == 0 ? first : second;
   const int64_t t = blockIdx.x;
   const int j0 = 4 * blockIdx.y;
   const int a = valid_id(job.index, t, job.count);
@@ -83,44 +84,61 @@ __global__ __launch_bounds__(256) void shrink_rows_kernel(ShrinkJob job, int64_t
   }
 }
 
-// v for 16 tokens per workgroup on v_mfma_f32_16x16x32_f16 (tokens x rank
+// v for 16 T tokens per workgroup on v_mfma_f32_16x16x32_f16 (tokens x rank
 // tiles of 16), the eight waves taking every eighth run of 32 of K and their
-// sums added in wave order.  One pass per adapter found among the 16 tokens.
+// sums added in wave order.  One pass per adapter found among the tokens.
 // Bound by the read of x: U runs are in flight per wave.
 constexpr int kShrinkWaves = 8;
-template <bool VEC, int NB, int U>
+template <bool VEC, int NB, int U, int T>
 __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_tile_kernel(ShrinkJob j0, ShrinkJob j1,
                                                                         int64_t m) {
   constexpr int W = kShrinkWaves;
-  __shared__ float red[W][16][16 * NB + 1];
+  __shared__ float red[W][16 * T][16 * NB + 1];
   const ShrinkJob& job = blockIdx.y == 0 ? j0 : j1;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, kg = lane >> 4;
-  const int64_t t0 = (int64_t)blockIdx.x * 16;
-  const int id = t0 + li < m ? valid_id(job.index, t0 + li, job.count) : -1;
-  const _Float16* x = job.x + min(t0 + li, m - 1) * job.ldx;
+  const int64_t t0 = (int64_t)blockIdx.x * 16 * T;
+  int id[T];
+  const _Float16* x[T];
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const int64_t tok = t0 + 16 * t + li;
+    id[t] = tok < m ? valid_id(job.index, tok, job.count) : -1;
+    x[t] = job.x + min(tok, m - 1) * job.ldx;
+  }
   // zeros where a token has no adapter, and behind the rank
-  for (int o = tid; o < 16 * job.ldv; o += 64 * W) {
+  for (int o = tid; o < 16 * T * job.ldv; o += 64 * W) {
     const int tok = o / job.ldv, j = o % job.ldv;
     if (t0 + tok < m && (j >= job.rank || valid_id(job.index, t0 + tok, job.count) < 0))
       job.v[(t0 + tok) * job.ldv + j] = 0.f;
   }
   int cur = -1;
   while (true) {
-    int next = id > cur ? id : 0x7fffffff;
+    int next = 0x7fffffff;
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+      if (id[t] > cur) next = min(next, id[t]);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) next = min(next, __shfl_xor(next, o, 64));
     cur = __builtin_amdgcn_readfirstlane(next);
     if (cur == 0x7fffffff) break;  // the same in all the waves
     const _Float16* down = job.down + cur * job.stride;
-    f32x4 acc[NB];
+    f32x4 acc[T][NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int64_t k0 = 32 * wave; k0 < job.K; k0 += 32 * W * U) {
-      half8 xv[U], dv[U][NB];
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // workgroups start at different columns: rows whose pitch is a multiple of
+    // 2 KB would have all of them read from the same memory channels
+    const int64_t turns = ceil_div(job.K, 32 * W * U);
+    int64_t turn = blockIdx.x % turns;
+    for (int64_t i = 0; i < turns; ++i, turn = turn + 1 == turns ? 0 : turn + 1) {
+      const int64_t k0 = 32 * wave + 32 * W * U * turn;
+      half8 xv[U][T], dv[U][NB];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t k = k0 + 32 * W * u + 8 * kg;
-        xv[u] = load8<VEC>(x, k, job.K);
+#pragma unroll
+        for (int t = 0; t < T; ++t) xv[u][t] = load8<VEC>(x[t], k, job.K);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const int j = 16 * b + li;  // a row of the adapter, zero behind the rank
@@ -131,17 +149,21 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_tile_kernel(ShrinkJo
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[u], dv[u][b], acc[b], 0, 0, 0);
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            acc[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[u][t], dv[u][b], acc[t][b], 0, 0, 0);
     }
     __syncthreads();  // the previous turn's reads of red
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int t = 0; t < T; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) red[wave][4 * kg + i][16 * b + li] = acc[b][i];
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) red[wave][16 * t + 4 * kg + i][16 * b + li] = acc[t][b][i];
     __syncthreads();
     const float s = job.scaling[cur];
-    for (int o = tid; o < 16 * 16 * NB; o += 64 * W) {
+    for (int o = tid; o < 16 * T * 16 * NB; o += 64 * W) {
       const int tok = o / (16 * NB), j = o % (16 * NB);
       if (t0 + tok < m && job.index[t0 + tok] == cur && j < job.rank) {
         float sum = 0.f;
@@ -150,84 +172,6 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_tile_kernel(ShrinkJo
         job.v[(t0 + tok) * job.ldv + j] = s * sum;
       }
     }
-  }
-}
-
-// B_a (rows x rank) -> rank x ldt, the rows' order along the fast axis, zeros
-// from rows to ldt: the layout the shrink kernels read.
-__global__ __launch_bounds__(256) void transpose_up_kernel(const _Float16* __restrict__ B,
-                                                           int64_t rows, int rank, int64_t ldt,
-                                                           _Float16* __restrict__ Bt) {
-  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t a = blockIdx.y;
-  if (n >= ldt) return;
-  for (int j = 0; j < rank; ++j)
-    Bt[(a * rank + j) * ldt + n] = n < rows ? B[(a * rows + n) * rank + j] : (_Float16)0.f;
-}
-
-// Tokens grouped by adapter, in token order inside each (so the gradients'
-// sums have one order), and cut into chunks of at most kGradChunk tokens of
-// one adapter.  One workgroup per adapter: it counts every adapter's tokens
-// (integer LDS atomics), finds its own places and writes its own tokens.
-__global__ __launch_bounds__(1024) void group_tokens_kernel(const int* __restrict__ index,
-                                                            int64_t m, int count, int max_chunks,
-                                                            int* __restrict__ list,
-                                                            GradChunk* __restrict__ chunks,
-                                                            int2* __restrict__ ranges) {
-  __shared__ int hist[kMaxGradAdapters];
-  __shared__ int wsum[16], base[2];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int a = blockIdx.x;
-  for (int i = tid; i < count; i += 1024) hist[i] = 0;
-  __syncthreads();
-  for (int64_t t = tid; t < m; t += 1024) {
-    const int d = valid_id(index, t, count);
-    if (d >= 0) atomicAdd(&hist[d], 1);
-  }
-  __syncthreads();
-  if (wave == 0) {  // tokens and chunks of the adapters before this one
-    int tokens = 0, before = 0, total = 0;
-    for (int i = lane; i < count; i += 64) {
-      const int c = (hist[i] + kGradChunk - 1) / kGradChunk;
-      total += c;
-      if (i < a) {
-        tokens += hist[i];
-        before += c;
-      }
-    }
-    for (int o = 32; o > 0; o >>= 1) {
-      tokens += __shfl_xor(tokens, o, 64);
-      before += __shfl_xor(before, o, 64);
-      total += __shfl_xor(total, o, 64);
-    }
-    const int mine = (hist[a] + kGradChunk - 1) / kGradChunk;
-    if (lane == 0) {
-      base[0] = tokens;
-      ranges[a] = make_int2(before, mine);
-    }
-    for (int c = lane; c < mine; c += 64)
-      chunks[before + c] = GradChunk{a, tokens + c * kGradChunk,
-                                     min(kGradChunk, hist[a] - c * kGradChunk)};
-    if (a == 0)
-      for (int c = total + lane; c < max_chunks; c += 64) chunks[c] = GradChunk{-1, 0, 0};
-  }
-  __syncthreads();
-  int at = base[0];
-  for (int64_t t0 = 0; t0 < m; t0 += 1024) {
-    const int64_t t = t0 + tid;
-    const bool mine = t < m && valid_id(index, t, count) == a;
-    const unsigned long long b = __ballot(mine);
-    if (lane == 0) wsum[wave] = __popcll(b);
-    __syncthreads();
-    int pre = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) {
-      if (w < wave) pre += wsum[w];
-      all += wsum[w];
-    }
-    if (mine) list[at + pre + __popcll(b & ((1ull << lane) - 1))] = (int)t;
-    at += all;
-    __syncthreads();
   }
 }
 
@@ -251,19 +195,51 @@ __global__ __launch_bounds__(256) void grad_chunk_kernel(GradJob g0, GradJob g1,
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[b][e] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < ch.count; k += 4) {
-    const bool in = k + kg < ch.count;
-    const int64_t t = list[ch.begin + min(k + kg, ch.count - 1)];
-    half8 r = {};
-    if (in) r = load8<VEC>(job.right + t * job.ldr, c0, job.N);
-    float l[NB];
+  // the chunk's tokens, 64 a register: no load of an index before a load of a row
+  static_assert(kGradChunk % 64 == 0, "token registers");
+  int tok[kGradChunk / 64];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) l[b] = in && 16 * (jb + b) < ldv ? job.left[t * ldv + 16 * (jb + b) + li] : 0.f;
+  for (int q = 0; q < kGradChunk / 64; ++q)
+    tok[q] = list[ch.begin + min(64 * q + lane, ch.count - 1)];
+  // U steps of four tokens are loaded while the U before them are used
+  constexpr int U = VEC ? (NB <= 2 ? 4 : 2) : 1;
+  half8 r[U];
+  float l[U][NB];
+  auto fetch = [&](int k0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + 4 * u + kg;
+      const bool in = k < ch.count;
+      const int q = (k0 + 4 * u) >> 6;  // uniform: 4 | k0
+      int mine = tok[0];
+#pragma unroll
+      for (int i = 1; i < kGradChunk / 64; ++i) mine = q == i ? tok[i] : mine;
+      const int64_t t = __shfl(mine, k & 63, 64);
+      r[u] = load8<VEC>(job.right + t * job.ldr, in ? c0 : job.N, job.N);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        acc[b][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(l[b], (float)r[e], acc[b][e], 0, 0, 0);
+        l[u][b] = in && 16 * (jb + b) < ldv ? job.left[t * ldv + 16 * (jb + b) + li] : 0.f;
+    }
+  };
+  fetch(0);
+  for (int k = 0; k < ch.count; k += 4 * U) {
+    half8 rc[U];
+    float lc[U][NB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      rc[u] = r[u];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) lc[u][b] = l[u][b];
+    }
+    if (k + 4 * U < ch.count) fetch(k + 4 * U);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          acc[b][e] =
+              __builtin_amdgcn_mfma_f32_16x16x4f32(lc[u][b], (float)rc[u][e], acc[b][e], 0, 0, 0);
   }
   float* out = job.part + (int64_t)blockIdx.y * rank * job.N;
 #pragma unroll
@@ -308,7 +284,16 @@ bool vec_job(const ShrinkJob& j) { return vec_ok(j.x, j.ldx, j.K) && vec_ok(j.do
 template <bool VEC, int NB>
 void shrink_tiles(const ShrinkJob& j0, const ShrinkJob* j1, int64_t m, hipStream_t s) {
   constexpr int U = !VEC ? 1 : NB <= 2 ? 4 : 2;
-  hipLaunchKernelGGL((shrink_tile_kernel<VEC, NB, U>),
+  // 32 tokens share an adapter row's load where that still fills the CUs
+  if constexpr (VEC && NB <= 2) {
+    if (m >= 32 * 256) {
+      hipLaunchKernelGGL((shrink_tile_kernel<VEC, NB, U, 2>),
+                         dim3((unsigned)ceil_div(m, 32), j1 ? 2 : 1), dim3(64 * kShrinkWaves), 0, s,
+                         j0, j1 ? *j1 : j0, m);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((shrink_tile_kernel<VEC, NB, U, 1>),
                      dim3((unsigned)ceil_div(m, 16), j1 ? 2 : 1), dim3(64 * kShrinkWaves), 0, s, j0,
                      j1 ? *j1 : j0, m);
 }
@@ -321,16 +306,17 @@ hipError_t launch_pack_x(const _Float16* x, int64_t ldx, int64_t m, int64_t K, _
   return hipGetLastError();
 }
 
-hipError_t launch_shrink_rows(const ShrinkJob& job, int64_t m, hipStream_t s) {
-  const dim3 grid((unsigned)m, (unsigned)(job.ldv / 4));
-  if (vec_job(job))
-    hipLaunchKernelGGL(shrink_rows_kernel<true>, grid, dim3(256), 0, s, job, m);
+static hipError_t launch_shrink_rows(const ShrinkJob& j0, const ShrinkJob* j1, int64_t m,
+                                     hipStream_t s) {
+  const dim3 grid((unsigned)m, (unsigned)(j0.ldv / 4), j1 ? 2 : 1);
+  if (vec_job(j0) && (j1 == nullptr || vec_job(*j1)))
+    hipLaunchKernelGGL(shrink_rows_kernel<true>, grid, dim3(256), 0, s, j0, j1 ? *j1 : j0);
   else
-    hipLaunchKernelGGL(shrink_rows_kernel<false>, grid, dim3(256), 0, s, job, m);
+    hipLaunchKernelGGL(shrink_rows_kernel<false>, grid, dim3(256), 0, s, j0, j1 ? *j1 : j0);
   return hipGetLastError();
 }
 
-hipError_t launch_shrink_tiles(const ShrinkJob& j0, const ShrinkJob* j1, int64_t m, hipStream_t s) {
+static hipError_t launch_shrink_tiles(const ShrinkJob& j0, const ShrinkJob* j1, int64_t m, hipStream_t s) {
   const bool vec = vec_job(j0) && (j1 == nullptr || vec_job(*j1));
   const int nb = j0.ldv / 16;
 #define GPTQ_SHRINK(V)                        \
@@ -347,21 +333,17 @@ hipError_t launch_shrink_tiles(const ShrinkJob& j0, const ShrinkJob* j1, int64_t
   return hipGetLastError();
 }
 
-hipError_t launch_transpose_up(const _Float16* B, int64_t count, int64_t rows, int rank,
-                               int64_t ldt, _Float16* Bt, hipStream_t s) {
-  hipLaunchKernelGGL(transpose_up_kernel, dim3((unsigned)ceil_div(ldt, 256), (unsigned)count),
-                     dim3(256), 0, s, B, rows, rank, ldt, Bt);
-  return hipGetLastError();
+// A few tokens have workgroups of their own: 16-token tiles leave CUs idle.
+// Per token that reads every adapter row again (rank + rank / 4 rows of K from
+// the L2), so the limit falls with the rank.
+hipError_t launch_shrink(const ShrinkJob& j0, const ShrinkJob* j1, int64_t m, hipStream_t s) {
+  if (m * j0.ldv <= 8192) return launch_shrink_rows(j0, j1, m, s);
+  const hipError_t e = launch_shrink_tiles(j0, j1, m, s);
+  if (e != hipSuccess || j0.xp == nullptr) return e;
+  return launch_pack_x(j0.x, j0.ldx, m, j0.K, j0.xp, s);
 }
 
 int64_t grad_chunks(int64_t m, int64_t count) { return ceil_div(m, kGradChunk) + count; }
-
-hipError_t launch_group_tokens(const int* index, int64_t m, int64_t count, int* list,
-                               GradChunk* chunks, int2* ranges, hipStream_t s) {
-  hipLaunchKernelGGL(group_tokens_kernel, dim3((unsigned)count), dim3(1024), 0, s, index, m,
-                     (int)count, (int)grad_chunks(m, count), list, chunks, ranges);
-  return hipGetLastError();
-}
 
 hipError_t launch_grads(const GradJob& g0, const GradJob& g1, int64_t m, int64_t count, int rank,
                         int ldv, const int* list, const GradChunk* chunks, const int2* ranges,

@@ -53,7 +53,9 @@ __device__ inline void add_adapters(f32x4 (&acc)[AT][BT], const AdapterTile& ad,
 #pragma unroll
     for (int a = 0; a < AT; ++a) {
       if (__ballot(id[a] == cur) == 0) continue;
-      const float* vrow = ad.v + min(t0 + 16 * a + li, m - 1) * ad.ldv + kg;
+      int row = 16 * a + li;
+      asm volatile("" : "+v"(row));  // keeps the AT row addresses out of the registers till here
+      const float* vrow = ad.v + min(t0 + row, m - 1) * ad.ldv + kg;
       f32x4 part[BT];
 #pragma unroll
       for (int b = 0; b < BT; ++b) part[b] = f32x4{0.f, 0.f, 0.f, 0.f};

@@ -123,18 +123,14 @@ struct ShrinkJob {
   int count, rank;
   float* v;
   int ldv;
-  _Float16* xp;  // launch_shrink_rows: if given, x also laid out as launch_pack_x does
+  _Float16* xp;  // if given (the first job): x also laid out as launch_pack_x does
 };
-// one workgroup per token and four j (a few tokens), or 16-token tiles of one
-// or two jobs of the same ldv
-hipError_t launch_shrink_rows(const ShrinkJob& job, int64_t m, hipStream_t s);
-hipError_t launch_shrink_tiles(const ShrinkJob& j0, const ShrinkJob* j1, int64_t m, hipStream_t s);
+// one or two jobs (of the same ldv)
+hipError_t launch_shrink(const ShrinkJob& j0, const ShrinkJob* j1, int64_t m, hipStream_t s);
 // xp: x (K % 128 == 0, 16-byte aligned rows) in 16-byte pieces of 8 columns:
 // [16-token tile][128-column chunk][32-column step][8-column piece][token]
 hipError_t launch_pack_x(const _Float16* x, int64_t ldx, int64_t m, int64_t K, _Float16* xp,
                          hipStream_t s);
-hipError_t launch_transpose_up(const _Float16* B, int64_t count, int64_t rows, int rank,
-                               int64_t ldt, _Float16* Bt, hipStream_t s);
 // out[a] = sum over the tokens t of adapter a of left[t][j] right[t][c]
 struct GradJob {
   const float* left;
@@ -150,8 +146,6 @@ struct GradChunk {
 constexpr int kGradChunk = 256;          // tokens per partial sum
 constexpr int kMaxGradAdapters = 4096;   // token counts held in LDS
 int64_t grad_chunks(int64_t m, int64_t count);
-hipError_t launch_group_tokens(const int* index, int64_t m, int64_t count, int* list,
-                               GradChunk* chunks, int2* ranges, hipStream_t s);
 hipError_t launch_grads(const GradJob& g0, const GradJob& g1, int64_t m, int64_t count, int rank,
                         int ldv, const int* list, const GradChunk* chunks, const int2* ranges,
                         hipStream_t s);
@@ -159,7 +153,7 @@ hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t s);
 constexpr int kMaxRank = 128;
 // the adapters' part of a product (adapters_dev.h)
 struct AdapterTile;
-// xp: x as launch_shrink_rows or launch_pack_x laid it out, where decode_mfma_ok
+// xp: x as launch_shrink or launch_pack_x laid it out, where decode_mfma_ok
 bool decode_mfma_ok(const _Float16* x, int64_t ldx, int64_t m, const uint32_t* packed, int bits,
                     int64_t cols, int groupsize, const int* g_idx);
 hipError_t launch_decode_adapters(const _Float16* x, const _Float16* xp, int64_t ldx, int64_t m,
@@ -184,10 +178,22 @@ int linear_splits(int bits, int64_t m, int64_t rows, int64_t cols, int groupsize
 // the transposed weights, cols x kp (kp >= rows a multiple of kKPad, zeros
 // behind the rows) with row pitch ldt, and the products with them
 constexpr int kKPad = 64;  // K of the fp16 product, padded with zeros
-hipError_t launch_dequant_transposed(const uint32_t* packed, int bits, int64_t rows, int64_t cols,
-                                     const float* scales, const float* zeros, int groupsize,
-                                     const int* g_idx, int64_t kp, int64_t ldt, _Float16* Wt,
-                                     hipStream_t s);
+struct PrepareAdapters {  // what the adapters' gradients need beside them
+  const _Float16* B;
+  int64_t count;
+  int rank;
+  int64_t ldb;      // Bt: count x rank x ldb, zeros behind the rows
+  _Float16* bt;
+  const int* index;
+  int64_t m;
+  int* list;
+  GradChunk* chunks;
+  int2* ranges;     // chunks of each adapter: first, number
+};
+hipError_t launch_prepare(const uint32_t* packed, int bits, int64_t rows, int64_t cols,
+                          const float* scales, const float* zeros, int groupsize, const int* g_idx,
+                          int64_t kp, int64_t ldt, _Float16* wt, const PrepareAdapters* ad,
+                          hipStream_t s);
 // dst[t][0 .. kp) = src[t][0 .. K) and zeros, row pitch ldd
 hipError_t launch_pad_rows(const _Float16* src, int64_t lds, int64_t m, int64_t K, int64_t kp,
                            int64_t ldd, _Float16* dst, hipStream_t s);

@@ -1,7 +1,6 @@
 // The gradient through a stored layer, dx = dy W_hat, and the products of the
 // vocabulary losses' gradient: the stored weights are written once in fp16
-// with the layer's outputs along the fast axis (launch_dequant_transposed),
-// and a dense fp16 product C = A B^T over that axis follows.
+// with the layer's outputs along the fast axis (launch_prepare), and a dense fp16 product C = A B^T over that axis follows.
 //
 // W_hat = (code - zero) * scale is formed in fp32 and rounded to fp16 once
 // (at most 2^-11 of its size, 2^-25 below 2^-14); the products are exact in
@@ -12,32 +11,58 @@
 namespace gptq {
 namespace {
 
-// ------------------------------------------------------- transposed weights
+// ------------------------------------------------------- what goes before
+// One launch writes the transposed weights and, for the adapters' gradients,
+// the transposed B and the tokens grouped by adapter: workgroups of one kind
+// after another, the grouping (a few long ones) first.
+struct Prepare {
+  // the layer
+  const uint32_t* packed;
+  int bits;
+  int64_t nw, rows, cols, kp;
+  const float *scales, *zeros;
+  int64_t ngroups;
+  int groupsize;
+  const int* g_idx;
+  int64_t ldt;
+  _Float16* wt;
+  // adapters (count 0: none)
+  const _Float16* B;
+  int64_t count;
+  int rank;
+  int64_t ldb;
+  _Float16* bt;
+  const int* index;
+  int64_t m;
+  int max_chunks;
+  int* list;
+  GradChunk* chunks;
+  int2* ranges;
+  int64_t bt_blocks, wt_x, wt_blocks;  // workgroups of each kind (wt_x per row of them)
+};
+
 // 4 and 8 bits, every word inside a group.  A lane takes one word of eight
 // adjacent rows (4 or 8 columns x 8 rows), so its outputs are whole 16-byte
 // pieces of the transposed rows; the lanes of a wave are eight such row groups
 // x eight words, which makes 128 adjacent bytes of eight rows per store.
-// Bound by the store: 90 MB at 11008 x 4096.
+// Bound by the store: 90 MB at 11008 x 4096, 34 us.
 template <int BITS>
-__global__ __launch_bounds__(256) void dequant_transposed_words_kernel(
-    const uint32_t* __restrict__ packed, int64_t nw, int64_t rows, int64_t cols, int64_t kp,
-    const float* __restrict__ scales, const float* __restrict__ zeros, int64_t ngroups,
-    int groupsize, int64_t ldt, _Float16* __restrict__ Wt) {
+__device__ inline void transpose_words(const Prepare& p, int64_t bx, int64_t by) {
   constexpr int K = 32 / BITS;
   constexpr uint32_t MASK = (1u << BITS) - 1u;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t r0 = (int64_t)blockIdx.x * 64 + 8 * (lane & 7);
-  const int64_t w = (int64_t)blockIdx.y * 32 + 8 * wave + (lane >> 3);
-  if (w >= nw || r0 >= kp) return;
-  const int64_t g = w * K / groupsize;
+  const int64_t r0 = bx * 64 + 8 * (lane & 7);
+  const int64_t w = by * 32 + 8 * wave + (lane >> 3);
+  if (w >= p.nw || r0 >= p.kp) return;
+  const int64_t g = w * K / p.groupsize;
   uint32_t q[8];
   float s[8], z[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int64_t r = min(r0 + i, rows - 1);
-    q[i] = packed[r * nw + w];
-    s[i] = scales[r * ngroups + g];
-    z[i] = zeros[r * ngroups + g];
+    const int64_t r = min(r0 + i, p.rows - 1);
+    q[i] = p.packed[r * p.nw + w];
+    s[i] = p.scales[r * p.ngroups + g];
+    z[i] = p.zeros[r * p.ngroups + g];
   }
 #pragma unroll
   for (int j = 0; j < K; ++j) {
@@ -45,37 +70,34 @@ __global__ __launch_bounds__(256) void dequant_transposed_words_kernel(
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float f = ((float)((q[i] >> (BITS * j)) & MASK) - z[i]) * s[i];
-      v[i] = (_Float16)(r0 + i < rows ? f : 0.f);
+      v[i] = (_Float16)(r0 + i < p.rows ? f : 0.f);
     }
-    if (w * K + j < cols) *reinterpret_cast<half8*>(Wt + (w * K + j) * ldt + r0) = v;
+    if (w * K + j < p.cols) *reinterpret_cast<half8*>(p.wt + (w * K + j) * p.ldt + r0) = v;
   }
 }
 
 // Any bits and groups: 64 rows x 64 columns per workgroup through LDS.
-__global__ __launch_bounds__(256) void dequant_transposed_kernel(
-    const uint32_t* __restrict__ packed, int bits, int64_t nw, int64_t rows, int64_t cols,
-    const float* __restrict__ scales, const float* __restrict__ zeros, int64_t ngroups,
-    int groupsize, const int* __restrict__ g_idx, int64_t ldt, _Float16* __restrict__ Wt) {
-  // (blockIdx.x covers the padded rows)
-  __shared__ __attribute__((aligned(16))) _Float16 tile[64][64 + 8];
-  const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
-  const int tid = threadIdx.x, k = 32 / bits;
-  const uint32_t mask = (1u << bits) - 1u;
+typedef _Float16 TransposeTile[64][64 + 8];
+__device__ inline void transpose_tile(const Prepare& p, int64_t bx, int64_t by,
+                                      TransposeTile& tile) {
+  const int64_t r0 = bx * 64, c0 = by * 64;
+  const int tid = threadIdx.x, k = 32 / p.bits;
+  const uint32_t mask = (1u << p.bits) - 1u;
   {
     const int64_t c = c0 + (tid & 63);
-    const int64_t cc = c < cols ? c : cols - 1;
-    int64_t g = g_idx != nullptr ? (int64_t)g_idx[cc] : cc / groupsize;
-    g = g < 0 ? 0 : g >= ngroups ? ngroups - 1 : g;
+    const int64_t cc = min(c, p.cols - 1);
+    int64_t g = p.g_idx != nullptr ? (int64_t)p.g_idx[cc] : cc / p.groupsize;
+    g = g < 0 ? 0 : g >= p.ngroups ? p.ngroups - 1 : g;
     const int64_t w = cc / k;
-    const int sh = bits * (int)(cc % k);
+    const int sh = p.bits * (int)(cc % k);
 #pragma unroll 4
     for (int i = 0; i < 16; ++i) {
       const int row = (tid >> 6) * 16 + i;
       const int64_t r = r0 + row;
       float v = 0.f;
-      if (r < rows && c < cols) {
-        const float q = (float)((packed[r * nw + w] >> sh) & mask);
-        v = (q - zeros[r * ngroups + g]) * scales[r * ngroups + g];
+      if (r < p.rows && c < p.cols) {
+        const float q = (float)((p.packed[r * p.nw + w] >> sh) & mask);
+        v = (q - p.zeros[r * p.ngroups + g]) * p.scales[r * p.ngroups + g];
       }
       tile[tid & 63][row] = (_Float16)v;
     }
@@ -83,11 +105,114 @@ __global__ __launch_bounds__(256) void dequant_transposed_kernel(
   __syncthreads();
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int o = tid + 256 * u, c = o >> 3, p = o & 7;
-    if (c0 + c < cols)
-      *reinterpret_cast<uint4*>(Wt + (c0 + c) * ldt + r0 + 8 * p) =
-          *reinterpret_cast<const uint4*>(&tile[c][8 * p]);
+    const int o = tid + 256 * u, c = o >> 3, q = o & 7;
+    if (c0 + c < p.cols)
+      *reinterpret_cast<uint4*>(p.wt + (c0 + c) * p.ldt + r0 + 8 * q) =
+          *reinterpret_cast<const uint4*>(&tile[c][8 * q]);
   }
+}
+
+// B_a (rows x rank) -> rank x ldb, the rows' order along the fast axis, zeros
+// from rows to ldb: the layout that v's kernels read.
+__device__ inline void transpose_up(const Prepare& p, int64_t bid) {
+  const int64_t per = ceil_div(p.ldb, 256);
+  const int64_t a = bid / per, n = (bid % per) * 256 + threadIdx.x;
+  if (n >= p.ldb) return;
+  for (int j = 0; j < p.rank; ++j)
+    p.bt[(a * p.rank + j) * p.ldb + n] =
+        n < p.rows ? p.B[(a * p.rows + n) * p.rank + j] : (_Float16)0.f;
+}
+
+// Tokens grouped by adapter, in token order inside each (so the gradients'
+// sums have one order), and cut into chunks of at most kGradChunk tokens of
+// one adapter.  One workgroup per adapter: it counts every adapter's tokens
+// (integer LDS atomics), finds its own places and writes its own tokens, 16
+// adjacent ones a thread at a time.
+struct GroupShared {
+  int hist[kMaxGradAdapters];
+  int wsum[4], base;
+};
+constexpr int kPerThread = 16;
+
+__device__ inline void group_tokens(const Prepare& p, int a, GroupShared& sh) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, count = (int)p.count;
+  for (int i = tid; i < count; i += 256) sh.hist[i] = 0;
+  __syncthreads();
+#pragma unroll 8
+  for (int64_t t = tid; t < p.m; t += 256) {
+    const int d = p.index[t];
+    if (d >= 0 && d < count) atomicAdd(&sh.hist[d], 1);
+  }
+  __syncthreads();
+  if (wave == 0) {  // tokens and chunks of the adapters before this one
+    int tokens = 0, before = 0, total = 0;
+    for (int i = lane; i < count; i += 64) {
+      const int c = (sh.hist[i] + kGradChunk - 1) / kGradChunk;
+      total += c;
+      if (i < a) {
+        tokens += sh.hist[i];
+        before += c;
+      }
+    }
+    for (int o = 32; o > 0; o >>= 1) {
+      tokens += __shfl_xor(tokens, o, 64);
+      before += __shfl_xor(before, o, 64);
+      total += __shfl_xor(total, o, 64);
+    }
+    const int mine = (sh.hist[a] + kGradChunk - 1) / kGradChunk;
+    if (lane == 0) {
+      sh.base = tokens;
+      p.ranges[a] = make_int2(before, mine);
+    }
+    for (int c = lane; c < mine; c += 64)
+      p.chunks[before + c] = GradChunk{a, tokens + c * kGradChunk,
+                                       min(kGradChunk, sh.hist[a] - c * kGradChunk)};
+    if (a == 0)
+      for (int c = total + lane; c < p.max_chunks; c += 64) p.chunks[c] = GradChunk{-1, 0, 0};
+  }
+  __syncthreads();
+  int at = sh.base;
+  for (int64_t t0 = 0; t0 < p.m; t0 += 256 * kPerThread) {
+    const int64_t first = t0 + tid * kPerThread;
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i)
+      if (first + i < p.m && p.index[first + i] == a) mine |= 1u << i;
+    int pre = __popc(mine);  // inclusive over the wave's lanes, then exclusive
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(pre, o, 64);
+      if (lane >= o) pre += v;
+    }
+    if (lane == 63) sh.wsum[wave] = pre;
+    __syncthreads();
+    int all = 0;
+    pre -= __popc(mine);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) pre += sh.wsum[w];
+      all += sh.wsum[w];
+    }
+    for (int i = 0, n = 0; i < kPerThread; ++i)
+      if (mine >> i & 1) p.list[at + pre + n++] = (int)(first + i);
+    at += all;
+    __syncthreads();
+  }
+}
+
+// WORDS: 4 or 8, the bits of the layer's word-wise transposition, else 0
+template <int WORDS>
+__global__ __launch_bounds__(256) void prepare_kernel(Prepare p) {
+  __shared__ union {
+    GroupShared group;
+    TransposeTile tile;
+  } sh;
+  int64_t bid = blockIdx.x;
+  if (bid < p.count) return group_tokens(p, (int)bid, sh.group);
+  bid -= p.count;
+  if (bid < p.bt_blocks) return transpose_up(p, bid);
+  bid -= p.bt_blocks;
+  if constexpr (WORDS > 0) transpose_words<WORDS>(p, bid % p.wt_x, bid / p.wt_x);
+  else transpose_tile(p, bid % p.wt_x, bid / p.wt_x, sh.tile);
 }
 
 __global__ __launch_bounds__(256) void pad_rows_kernel(const _Float16* __restrict__ src,
@@ -332,22 +457,46 @@ int gemm_splits(int64_t m, int64_t n, int64_t K) {
   return s < 2 ? 1 : (int)s;
 }
 
-hipError_t launch_dequant_transposed(const uint32_t* packed, int bits, int64_t rows, int64_t cols,
-                                     const float* scales, const float* zeros, int groupsize,
-                                     const int* g_idx, int64_t kp, int64_t ldt, _Float16* Wt,
-                                     hipStream_t s) {
-  const int64_t nw = packed_words(cols, bits), ng = ceil_div(cols, groupsize);
-  const dim3 words((unsigned)(kp / 64), (unsigned)ceil_div(nw, 32));
-  if (bits == 4 && g_idx == nullptr && (groupsize % 8 == 0 || groupsize >= cols))
-    hipLaunchKernelGGL(dequant_transposed_words_kernel<4>, words, dim3(256), 0, s, packed, nw, rows,
-                       cols, kp, scales, zeros, ng, groupsize, ldt, Wt);
-  else if (bits == 8 && g_idx == nullptr && (groupsize % 4 == 0 || groupsize >= cols))
-    hipLaunchKernelGGL(dequant_transposed_words_kernel<8>, words, dim3(256), 0, s, packed, nw, rows,
-                       cols, kp, scales, zeros, ng, groupsize, ldt, Wt);
-  else
-    hipLaunchKernelGGL(dequant_transposed_kernel,
-                       dim3((unsigned)(kp / 64), (unsigned)ceil_div(cols, 64)), dim3(256), 0, s,
-                       packed, bits, nw, rows, cols, scales, zeros, ng, groupsize, g_idx, ldt, Wt);
+hipError_t launch_prepare(const uint32_t* packed, int bits, int64_t rows, int64_t cols,
+                          const float* scales, const float* zeros, int groupsize, const int* g_idx,
+                          int64_t kp, int64_t ldt, _Float16* wt, const PrepareAdapters* ad,
+                          hipStream_t s) {
+  Prepare p{};
+  p.packed = packed;
+  p.bits = bits;
+  p.nw = packed_words(cols, bits);
+  p.rows = rows;
+  p.cols = cols;
+  p.kp = kp;
+  p.scales = scales;
+  p.zeros = zeros;
+  p.ngroups = ceil_div(cols, groupsize);
+  p.groupsize = groupsize;
+  p.g_idx = g_idx;
+  p.ldt = ldt;
+  p.wt = wt;
+  if (ad != nullptr) {
+    p.B = ad->B;
+    p.count = ad->count;
+    p.rank = ad->rank;
+    p.ldb = ad->ldb;
+    p.bt = ad->bt;
+    p.index = ad->index;
+    p.m = ad->m;
+    p.max_chunks = (int)grad_chunks(ad->m, ad->count);
+    p.list = ad->list;
+    p.chunks = ad->chunks;
+    p.ranges = ad->ranges;
+    p.bt_blocks = ad->count * ceil_div(ad->ldb, 256);
+  }
+  const bool words = g_idx == nullptr && (bits == 4 || bits == 8) &&
+                     (groupsize % (32 / bits) == 0 || groupsize >= cols);
+  p.wt_x = kp / 64;
+  p.wt_blocks = p.wt_x * (words ? ceil_div(p.nw, 32) : ceil_div(cols, 64));
+  const dim3 grid((unsigned)(p.count + p.bt_blocks + p.wt_blocks));
+  if (words && bits == 4) hipLaunchKernelGGL(prepare_kernel<4>, grid, dim3(256), 0, s, p);
+  else if (words) hipLaunchKernelGGL(prepare_kernel<8>, grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL(prepare_kernel<0>, grid, dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

@@ -184,16 +184,6 @@ AdapterTile forward_tile(const gptq_adapters* ad, int64_t rows, const float* v) 
   return t;
 }
 
-// A few tokens have workgroups of their own: 16-token tiles leave CUs idle.
-// Per token that reads every adapter row again (rank + rank / 4 rows of K from
-// the L2), so the limit falls with the rank.
-hipError_t shrink(const ShrinkJob& job, int64_t m, hipStream_t s) {
-  if (m * job.ldv <= 8192) return launch_shrink_rows(job, m, s);
-  const hipError_t e = launch_shrink_tiles(job, nullptr, m, s);
-  if (e != hipSuccess || job.xp == nullptr) return e;
-  return launch_pack_x(job.x, job.ldx, m, job.K, job.xp, s);
-}
-
 #define GPTQ_TRY(call)                             \
   do {                                             \
     if ((call) != hipSuccess) return GPTQ_ERR_HIP; \
@@ -242,7 +232,7 @@ gptq_status gptq_dequant_gemm_adapters(const void* x, int64_t m, int64_t cols, i
   if (decode_mfma_ok(xh, ldx, m, packed, bits, cols, groupsize, g_idx))
     job.xp = reinterpret_cast<_Float16*>(reinterpret_cast<char*>(workspace) +
                                          forward_v_bytes(m, ad->rank));
-  GPTQ_TRY(shrink(job, m, s));
+  GPTQ_TRY(launch_shrink(job, nullptr, m, s));
   GPTQ_TRY(launch_decode_adapters(xh, job.xp, ldx, m, packed, bits, rows,
                                   cols, scales, zeros, groupsize, g_idx, forward_tile(ad, rows, v),
                                   y, ldy, s));
@@ -268,7 +258,7 @@ gptq_status gptq_linear_forward_adapters(const void* x, int64_t m, int64_t cols,
   if (ok != GPTQ_OK) return ok;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   float* v = reinterpret_cast<float*>(workspace);
-  GPTQ_TRY(shrink(forward_job(ad, x, ldx, cols, v), m, s));
+  GPTQ_TRY(launch_shrink(forward_job(ad, x, ldx, cols, v), nullptr, m, s));
   GPTQ_TRY(launch_linear_forward_adapters(bits, reinterpret_cast<const _Float16*>(x), ldx, m,
                                           packed, rows, cols, scales, zeros, groupsize, relu == 1,
                                           forward_tile(ad, rows, v),
@@ -317,8 +307,6 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
     g = p;
     ldg = L.ldt;
   }
-  GPTQ_TRY(launch_dequant_transposed(packed, bits, rows, cols, scales, zeros, groupsize, g_idx, L.kp,
-                                     L.ldt, wt, s));
   AdapterTile tile{};
   if (ad != nullptr) {
     float* v = reinterpret_cast<float*>(ws + L.v);
@@ -328,9 +316,10 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
     GradChunk* chunks = reinterpret_cast<GradChunk*>(ws + L.chunks);
     int2* ranges = reinterpret_cast<int2*>(ws + L.ranges);
     const int64_t ldt = round_up(rows, 8);
-    GPTQ_TRY(launch_transpose_up(reinterpret_cast<const _Float16*>(ad->B), count, rows, rank, ldt,
-                                 bt, s));
-    GPTQ_TRY(launch_group_tokens(ad->index, m, count, list, chunks, ranges, s));
+    const PrepareAdapters pa{reinterpret_cast<const _Float16*>(ad->B), count, rank, ldt, bt,
+                             ad->index, m, list, chunks, ranges};
+    GPTQ_TRY(launch_prepare(packed, bits, rows, cols, scales, zeros, groupsize, g_idx, L.kp, L.ldt,
+                            wt, &pa, s));
     const ShrinkJob jx = forward_job(ad, x, ldx, cols, v);
     ShrinkJob jy = jx;  // dv = s dy B, over the rows
     jy.x = g;
@@ -340,7 +329,7 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
     jy.ldd = ldt;
     jy.stride = rank * ldt;
     jy.v = dv;
-    GPTQ_TRY(launch_shrink_tiles(jx, &jy, m, s));
+    GPTQ_TRY(launch_shrink(jx, &jy, m, s));
     GradJob ga{}, gb{};
     ga.left = dv;
     ga.right = reinterpret_cast<const _Float16*>(x);
@@ -364,6 +353,9 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
     tile.stride = rank * cols;
     tile.js = cols;
     tile.ns = 1;
+  } else {
+    GPTQ_TRY(launch_prepare(packed, bits, rows, cols, scales, zeros, groupsize, g_idx, L.kp, L.ldt,
+                            wt, nullptr, s));
   }
   GPTQ_TRY(launch_gemm_nt_f16(g, ldg, m, wt, L.ldt, cols, L.kp, ad != nullptr ? &tile : nullptr,
                               reinterpret_cast<float*>(ws + L.sums),
@@ -472,8 +464,8 @@ gptq_status head_backward(const void* h, int64_t m, int64_t cols, int64_t ldh,
       GPTQ_TRY(launch_head_probs(bits, x, ldh, mt, packed + v0 * nw, w, cols, scales + v0 * ng,
                                  zeros + v0 * ng, groupsize, tg.inv_t, lse_eff + t0, P, ld, s));
       GPTQ_TRY(launch_head_scatter(tt, mt, rows, v0, w, zk + t0 * top, lse + t0, P, ld, s));
-      GPTQ_TRY(launch_dequant_transposed(packed + v0 * nw, bits, w, cols, scales + v0 * ng,
-                                         zeros + v0 * ng, groupsize, nullptr, wp, ld, wt, s));
+      GPTQ_TRY(launch_prepare(packed + v0 * nw, bits, w, cols, scales + v0 * ng, zeros + v0 * ng,
+                              groupsize, nullptr, wp, ld, wt, nullptr, s));
       GPTQ_TRY(launch_gemm_nt_acc(P, ld, mt, wt, ld, cols, wp, v0 == 0, acc, gscale + t0,
                                   reinterpret_cast<float*>(ws + L.sums), last ? out : nullptr, lddh,
                                   s));
