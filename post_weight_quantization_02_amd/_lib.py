@@ -7,6 +7,7 @@ built, importing this module raises ImportError: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -498,73 +499,122 @@ def linear_forward(x, packed, bits: int, cols: int, scales, zeros, groupsize: in
 
 
 # ------------------------------------------- adapters, gradients, vocabulary losses
+# These calls are short enough on the GPU (a decode step of one token: 9 us)
+# for their checks to count: tensors are compared by dtype identity, shape and
+# device index, and workspace sizes, which depend on the sizes alone, are kept.
+_f16, _f32, _i32 = torch.float16, torch.float32, torch.int32
+# the current stream's handle without a Stream object (2 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+@functools.lru_cache(maxsize=1024)
 def adapters_workspace_bytes(op: int, m: int, rows: int, cols: int, count: int = 0,
                              rank: int = 0) -> int:
     """Workspace of OP_FORWARD_ADAPTERS or OP_BACKWARD for m tokens."""
     return int(lib.gptq_adapters_workspace_bytes(op, m, rows, cols, count, rank))
 
 
+@functools.lru_cache(maxsize=1024)
 def head_workspace_bytes(op: int, m: int, rows: int, cols: int) -> int:
     """Workspace of OP_HEAD_LOSS or OP_HEAD_BACKWARD for m tokens."""
     return int(lib.gptq_head_workspace_bytes(op, m, rows, cols))
 
 
-def _rows_of(t, m, n, dtype, device, name):
-    """An m x n matrix with unit column stride; returns its row stride."""
-    if t.dtype != dtype or t.device != device or t.dim() != 2 or tuple(t.shape) != (m, n) or \
+def _rows_of(t, m, n, dtype, dev, name):
+    """An m x n matrix with unit column stride on GPU dev; returns its row stride."""
+    if t.dtype is not dtype or t.shape != (m, n) or t.get_device() != dev or \
             (n > 1 and m > 0 and t.stride(1) != 1):
         raise ValueError(f"{name} must be an {m} x {n} {dtype} tensor with unit column stride "
-                         f"on {device}")
+                         f"on cuda:{dev}")
     return t.stride(0) if m > 1 else n
 
 
-def _layer(packed, bits, cols, scales, zeros, groupsize, device, g_idx=None):
-    """The stored layer's checks; returns (rows, groupsize, g_idx)."""
-    torch = _torch()
-    if packed.dim() != 2 or packed.dtype != torch.int32 or not packed.is_contiguous() or \
-            packed.device != device or packed.shape[1] != packed_words(cols, bits):
+def _exactly(t, shape, dtype, dev, name):
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} "
+                         f"on cuda:{dev}")
+
+
+def _input(x, n, name):
+    """(tokens, row stride, GPU index) of an fp16 input with n columns."""
+    if x.dtype is not _f16 or x.dim() != 2 or not x.is_cuda or n is not None and x.shape[1] != n:
+        raise ValueError(f"{name} must be a 2-D fp16 CUDA tensor with unit column stride"
+                         + ("" if n is None else f" and {n} columns"))
+    dev, (m, n) = x.get_device(), x.shape
+    return m, _rows_of(x, m, n, _f16, dev, name), dev
+
+
+def _layer(packed, bits, cols, scales, zeros, groupsize, dev, g_idx=None):
+    """The stored layer's checks; returns (rows, groupsize)."""
+    if packed.dtype is not _i32 or packed.dim() != 2 or not packed.is_contiguous() or \
+            packed.get_device() != dev or not 2 <= bits <= 8 or \
+            packed.shape[1] != -(-cols // (32 // bits)):
         raise ValueError("packed must come from pack_codes for these cols and bits")
     rows = packed.shape[0]
     if groupsize <= 0:
         groupsize = cols
-    ng = (cols + groupsize - 1) // groupsize
-    for t in (scales, zeros):
-        if t.dtype != torch.float32 or tuple(t.shape) != (rows, ng) or not t.is_contiguous() or \
-                t.device != device:
-            raise ValueError("scales and zeros must be contiguous rows x ngroups fp32")
-    return rows, groupsize, _check_perm(g_idx, cols, device)
+    shape = (rows, -(-cols // groupsize))
+    _exactly(scales, shape, _f32, dev, "scales")
+    _exactly(zeros, shape, _f32, dev, "zeros")
+    if g_idx is not None:
+        _exactly(g_idx, (cols,), _i32, dev, "g_idx")
+    return rows, groupsize
 
 
-def _adapters(A, B, scaling, index, m, rows, cols, device):
+def _adapters(A, B, scaling, index, m, rows, cols, dev):
     """The adapters' checks; returns the C struct."""
-    torch = _torch()
-    if A.dim() != 3 or B.dim() != 3:
+    if A.dim() != 3:
         raise ValueError("A must be count x rank x cols and B count x rows x rank")
     count, rank = A.shape[0], A.shape[1]
-    for t, shape, dtype, name in ((A, (count, rank, cols), torch.float16, "A"),
-                                  (B, (count, rows, rank), torch.float16, "B"),
-                                  (scaling, (count,), torch.float32, "scaling"),
-                                  (index, (m,), torch.int32, "index")):
-        if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or \
-                not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} "
-                             f"on {device}")
+    _exactly(A, (count, rank, cols), _f16, dev, "A")
+    _exactly(B, (count, rows, rank), _f16, dev, "B")
+    _exactly(scaling, (count,), _f32, dev, "scaling")
+    _exactly(index, (m,), _i32, dev, "index")
     return _Adapters(A.data_ptr(), B.data_ptr(), scaling.data_ptr(), index.data_ptr(), count, rank)
 
 
-def _out_rows(out, m, n, dtype, device):
+def _out_rows(out, m, n, dtype, dev):
     """(out, its row stride), allocated when None."""
-    torch = _torch()
     if out is None:
-        out = torch.empty((m, n), dtype=dtype, device=device)
-    return out, _rows_of(out, m, n, dtype, device, "out")
+        return torch.empty((m, n), dtype=dtype, device=dev), n
+    return out, _rows_of(out, m, n, dtype, dev, "out")
 
 
-def _x_rows(x, cols, name="x"):
-    torch = _torch()
-    if x.dtype != torch.float16 or not x.is_cuda or x.dim() != 2 or x.shape[1] != cols:
-        raise ValueError(f"{name} must be an m x cols fp16 CUDA tensor with unit column stride")
-    return x.shape[0], _rows_of(x, x.shape[0], cols, torch.float16, x.device, name)
+def _out_exactly(out, shape, dtype, dev, name):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _exactly(out, shape, dtype, dev, name)
+    return out
+
+
+def _launch(fn, args, nbytes, dev, workspace, stream):
+    """fn(*args, workspace, bytes, stream) on GPU dev; raises its errors."""
+    ws = None
+    if nbytes > 0:
+        if workspace is None:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            if ws.data_ptr() % 256:  # another allocator than torch's own
+                ws, _ = _workspace(nbytes, ws.device)
+            if stream is not None:
+                # freed on return: the allocator must not hand it on before
+                # the work queued on `stream` is done
+                ws.record_stream(stream)
+        else:
+            ws, nbytes = _workspace(nbytes, torch.device("cuda", dev), workspace, stream)
+    if stream is not None:
+        handle = stream.cuda_stream
+    elif _raw_stream is not None:
+        handle = _raw_stream(dev)
+    else:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    args = (*args, ws.data_ptr() if ws is not None else None, nbytes, handle)
+    if torch.cuda.current_device() == dev:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args)
+    if status != GPTQ_OK:
+        raise GPTQError(status, fn.__name__)
 
 
 def dequant_gemm_adapters(x, packed, bits: int, cols: int, scales, zeros, groupsize: int, A, B,
@@ -573,20 +623,16 @@ def dequant_gemm_adapters(x, packed, bits: int, cols: int, scales, zeros, groups
     y_t += scaling[a] B[a] (A[a] x_t), a = index[t]; an index outside
     [0, count) adds nothing. A: count x rank x cols and B: count x rows x rank
     fp16, scaling: count fp32, index: m int32 (gptq_dequant_gemm_adapters)."""
-    torch = _torch()
-    m, ldx = _x_rows(x, cols)
-    rows, groupsize, g_idx = _layer(packed, bits, cols, scales, zeros, groupsize, x.device, g_idx)
-    ad = _adapters(A, B, scaling, index, m, rows, cols, x.device)
-    out, ldy = _out_rows(out, m, rows, torch.float32, x.device)
-    ws, wsb = _workspace(adapters_workspace_bytes(OP_FORWARD_ADAPTERS, m, rows, cols, ad.count,
-                                                  ad.rank), x.device, workspace, stream)
-    with torch.cuda.device(x.device):
-        st = lib.gptq_dequant_gemm_adapters(
-            x.data_ptr(), m, cols, ldx, packed.data_ptr(), bits, rows, scales.data_ptr(),
-            zeros.data_ptr(), groupsize, g_idx.data_ptr() if g_idx is not None else None,
-            ctypes.byref(ad), out.data_ptr(), ldy, ws.data_ptr() if ws is not None else None, wsb,
-            _stream_ptr(stream, x.device))
-    _check(st, "gptq_dequant_gemm_adapters")
+    m, ldx, dev = _input(x, cols, "x")
+    rows, groupsize = _layer(packed, bits, cols, scales, zeros, groupsize, dev, g_idx)
+    ad = _adapters(A, B, scaling, index, m, rows, cols, dev)
+    out, ldy = _out_rows(out, m, rows, _f32, dev)
+    _launch(lib.gptq_dequant_gemm_adapters,
+            (x.data_ptr(), m, cols, ldx, packed.data_ptr(), bits, rows, scales.data_ptr(),
+             zeros.data_ptr(), groupsize, g_idx.data_ptr() if g_idx is not None else None, ad,
+             out.data_ptr(), ldy),
+            adapters_workspace_bytes(OP_FORWARD_ADAPTERS, m, rows, cols, ad.count, ad.rank), dev,
+            workspace, stream)
     return out
 
 
@@ -595,62 +641,32 @@ def linear_forward_adapters(x, packed, bits: int, cols: int, scales, zeros, grou
                             stream=None):
     """linear_forward (m x rows fp16, many tokens) with each token's low-rank
     adapter, as dequant_gemm_adapters (gptq_linear_forward_adapters)."""
-    torch = _torch()
-    m, ldx = _x_rows(x, cols)
-    rows, groupsize, _ = _layer(packed, bits, cols, scales, zeros, groupsize, x.device)
-    ad = _adapters(A, B, scaling, index, m, rows, cols, x.device)
-    out, ldy = _out_rows(out, m, rows, torch.float16, x.device)
-    ws, wsb = _workspace(adapters_workspace_bytes(OP_FORWARD_ADAPTERS, m, rows, cols, ad.count,
-                                                  ad.rank), x.device, workspace, stream)
-    with torch.cuda.device(x.device):
-        st = lib.gptq_linear_forward_adapters(
-            x.data_ptr(), m, cols, ldx, packed.data_ptr(), bits, rows, scales.data_ptr(),
-            zeros.data_ptr(), groupsize, 1 if relu else 0, ctypes.byref(ad), out.data_ptr(), ldy,
-            ws.data_ptr() if ws is not None else None, wsb, _stream_ptr(stream, x.device))
-    _check(st, "gptq_linear_forward_adapters")
+    m, ldx, dev = _input(x, cols, "x")
+    rows, groupsize = _layer(packed, bits, cols, scales, zeros, groupsize, dev)
+    ad = _adapters(A, B, scaling, index, m, rows, cols, dev)
+    out, ldy = _out_rows(out, m, rows, _f16, dev)
+    _launch(lib.gptq_linear_forward_adapters,
+            (x.data_ptr(), m, cols, ldx, packed.data_ptr(), bits, rows, scales.data_ptr(),
+             zeros.data_ptr(), groupsize, 1 if relu else 0, ad, out.data_ptr(), ldy),
+            adapters_workspace_bytes(OP_FORWARD_ADAPTERS, m, rows, cols, ad.count, ad.rank), dev,
+            workspace, stream)
     return out
-
-
-def _backward(dy, x, layer, adapters, g_idx, out, dA, dB, workspace, stream):
-    torch = _torch()
-    packed, bits, cols, scales, zeros, groupsize = layer
-    if dy.dtype != torch.float16 or not dy.is_cuda or dy.dim() != 2:
-        raise ValueError("dy must be an m x rows fp16 CUDA tensor with unit column stride")
-    m, dev = dy.shape[0], dy.device
-    rows, groupsize, g_idx = _layer(packed, bits, cols, scales, zeros, groupsize, dev, g_idx)
-    lddy = _rows_of(dy, m, rows, torch.float16, dev, "dy")
-    out, lddx = _out_rows(out, m, cols, torch.float16, dev)
-    ad, ldx, count, rank = None, 0, 0, 0
-    if adapters is not None:
-        ldx = _rows_of(x, m, cols, torch.float16, dev, "x")
-        ad = _adapters(*adapters, m, rows, cols, dev)
-        count, rank = ad.count, ad.rank
-        if dA is None:
-            dA = torch.empty((count, rank, cols), dtype=torch.float32, device=dev)
-        if dB is None:
-            dB = torch.empty((count, rows, rank), dtype=torch.float32, device=dev)
-        _check_out(dA, (count, rank, cols), torch.float32, dev, "dA")
-        _check_out(dB, (count, rows, rank), torch.float32, dev, "dB")
-    ws, wsb = _workspace(adapters_workspace_bytes(OP_BACKWARD, m, rows, cols, count, rank), dev,
-                         workspace, stream)
-    with torch.cuda.device(dev):
-        st = lib.gptq_linear_backward(
-            dy.data_ptr(), m, rows, lddy, packed.data_ptr(), bits, cols, scales.data_ptr(),
-            zeros.data_ptr(), groupsize, g_idx.data_ptr() if g_idx is not None else None,
-            ctypes.byref(ad) if ad is not None else None, x.data_ptr() if ad is not None else None,
-            ldx, out.data_ptr(), lddx, dA.data_ptr() if ad is not None else None,
-            dB.data_ptr() if ad is not None else None, ws.data_ptr() if ws is not None else None,
-            wsb, _stream_ptr(stream, dev))
-    _check(st, "gptq_linear_backward")
-    return out, dA, dB
 
 
 def linear_backward(dy, packed, bits: int, cols: int, scales, zeros, groupsize: int, g_idx=None,
                     out=None, workspace=None, stream=None):
     """dx = dy W_hat (m x cols fp16) for dy m x rows fp16: the gradient
     through a stored layer (gptq_linear_backward without adapters)."""
-    return _backward(dy, None, (packed, bits, cols, scales, zeros, groupsize), None, g_idx, out,
-                     None, None, workspace, stream)[0]
+    m, lddy, dev = _input(dy, None, "dy")
+    rows, groupsize = _layer(packed, bits, cols, scales, zeros, groupsize, dev, g_idx)
+    _rows_of(dy, m, rows, _f16, dev, "dy")
+    out, lddx = _out_rows(out, m, cols, _f16, dev)
+    _launch(lib.gptq_linear_backward,
+            (dy.data_ptr(), m, rows, lddy, packed.data_ptr(), bits, cols, scales.data_ptr(),
+             zeros.data_ptr(), groupsize, g_idx.data_ptr() if g_idx is not None else None, None,
+             None, 0, out.data_ptr(), lddx, None, None),
+            adapters_workspace_bytes(OP_BACKWARD, m, rows, cols), dev, workspace, stream)
+    return out
 
 
 def linear_backward_adapters(dy, x, packed, bits: int, cols: int, scales, zeros, groupsize: int, A,
@@ -660,84 +676,72 @@ def linear_backward_adapters(dy, x, packed, bits: int, cols: int, scales, zeros,
     fp32) of the product with adapters for its input x and dy (m x rows fp16);
     where the forward product had relu, dy is zero where its output is 0
     (gptq_linear_backward)."""
-    return _backward(dy, x, (packed, bits, cols, scales, zeros, groupsize),
-                     (A, B, scaling, index), g_idx, out, dA, dB, workspace, stream)
+    m, lddy, dev = _input(dy, None, "dy")
+    rows, groupsize = _layer(packed, bits, cols, scales, zeros, groupsize, dev, g_idx)
+    _rows_of(dy, m, rows, _f16, dev, "dy")
+    ldx = _rows_of(x, m, cols, _f16, dev, "x")
+    ad = _adapters(A, B, scaling, index, m, rows, cols, dev)
+    out, lddx = _out_rows(out, m, cols, _f16, dev)
+    dA = _out_exactly(dA, tuple(A.shape), _f32, dev, "dA")
+    dB = _out_exactly(dB, tuple(B.shape), _f32, dev, "dB")
+    _launch(lib.gptq_linear_backward,
+            (dy.data_ptr(), m, rows, lddy, packed.data_ptr(), bits, cols, scales.data_ptr(),
+             zeros.data_ptr(), groupsize, g_idx.data_ptr() if g_idx is not None else None, ad,
+             x.data_ptr(), ldx, out.data_ptr(), lddx, dA.data_ptr(), dB.data_ptr()),
+            adapters_workspace_bytes(OP_BACKWARD, m, rows, cols, ad.count, ad.rank), dev, workspace,
+            stream)
+    return out, dA, dB
 
 
-def _head_targets(index, logits, m, device):
-    """(top, checked tensors) of labels (logits None) or of a teacher's entries."""
-    torch = _torch()
+def _head_entries(index, logits, m, dev):
+    """The checks of labels (logits None: m) or of a teacher's entries (m x
+    top); returns the shape of the entries' logits."""
     if logits is None:
-        if index.dtype != torch.int32 or tuple(index.shape) != (m,) or index.device != device or \
-                not index.is_contiguous():
-            raise ValueError(f"target must be a contiguous int32 tensor of length {m} on {device}")
-        return 1
+        _exactly(index, (m,), _i32, dev, "target")
+        return (m,)
     if index.dim() != 2:
         raise ValueError("top_index must be m x top")
     shape = (m, index.shape[1])
-    for t, dtype, name in ((index, torch.int32, "top_index"), (logits, torch.float32, "top_logits")):
-        if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or \
-                not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous m x top {dtype} tensor on {device}")
-    return shape[1]
+    _exactly(index, shape, _i32, dev, "top_index")
+    _exactly(logits, shape, _f32, dev, "top_logits")
+    return shape
 
 
-def _head_forward(h, layer, index, logits, temperature, loss, lse, zk, workspace, stream):
-    torch = _torch()
+def _temperature(t):
+    t = float(t)
+    if not 1e-30 < t < 1e30:
+        raise ValueError("temperature must be positive")
+    return t
+
+
+def _head_forward(fn, h, layer, index, logits, more, loss, lse, zk, workspace, stream):
     packed, bits, cols, scales, zeros, groupsize = layer
-    m, ldh = _x_rows(h, cols, "h")
-    dev = h.device
-    rows, groupsize, _ = _layer(packed, bits, cols, scales, zeros, groupsize, dev)
-    top = _head_targets(index, logits, m, dev)
-    shape = (m,) if logits is None else (m, top)
-    if loss is None:
-        loss = torch.empty((m,), dtype=torch.float32, device=dev)
-    if lse is None:
-        lse = torch.empty((m,), dtype=torch.float32, device=dev)
-    if zk is None:
-        zk = torch.empty(shape, dtype=torch.float32, device=dev)
-    _check_out(loss, (m,), torch.float32, dev, "loss")
-    _check_out(lse, (m,), torch.float32, dev, "lse")
-    _check_out(zk, shape, torch.float32, dev, "the entries' logits")
-    ws, wsb = _workspace(head_workspace_bytes(OP_HEAD_LOSS, m, rows, cols), dev, workspace, stream)
-    head = (h.data_ptr(), m, cols, ldh, packed.data_ptr(), bits, rows, scales.data_ptr(),
-            zeros.data_ptr(), groupsize, index.data_ptr())
-    tail = (loss.data_ptr(), lse.data_ptr(), zk.data_ptr(),
-            ws.data_ptr() if ws is not None else None, wsb, _stream_ptr(stream, dev))
-    with torch.cuda.device(dev):
-        if logits is None:
-            st, name = lib.gptq_head_loss(*head, *tail), "gptq_head_loss"
-        else:
-            st = lib.gptq_head_distill(*head, logits.data_ptr(), top, temperature, *tail)
-            name = "gptq_head_distill"
-    _check(st, name)
+    m, ldh, dev = _input(h, cols, "h")
+    rows, groupsize = _layer(packed, bits, cols, scales, zeros, groupsize, dev)
+    shape = _head_entries(index, logits, m, dev)
+    loss = _out_exactly(loss, (m,), _f32, dev, "loss")
+    lse = _out_exactly(lse, (m,), _f32, dev, "lse")
+    zk = _out_exactly(zk, shape, _f32, dev, "the entries' logits")
+    _launch(fn, (h.data_ptr(), m, cols, ldh, packed.data_ptr(), bits, rows, scales.data_ptr(),
+                 zeros.data_ptr(), groupsize, index.data_ptr(), *more, loss.data_ptr(),
+                 lse.data_ptr(), zk.data_ptr()),
+            head_workspace_bytes(OP_HEAD_LOSS, m, rows, cols), dev, workspace, stream)
     return loss, lse, zk
 
 
-def _head_backward(h, layer, index, logits, temperature, lse, zk, dloss, out, workspace, stream):
-    torch = _torch()
+def _head_backward(fn, h, layer, index, logits, more, lse, zk, dloss, out, workspace, stream):
     packed, bits, cols, scales, zeros, groupsize = layer
-    m, ldh = _x_rows(h, cols, "h")
-    dev = h.device
-    rows, groupsize, _ = _layer(packed, bits, cols, scales, zeros, groupsize, dev)
-    top = _head_targets(index, logits, m, dev)
-    _check_out(lse, (m,), torch.float32, dev, "lse")
-    _check_out(zk, (m,) if logits is None else (m, top), torch.float32, dev, "the entries' logits")
-    _check_out(dloss, (m,), torch.float32, dev, "dloss")
-    out, lddh = _out_rows(out, m, cols, torch.float16, dev)
-    ws, wsb = _workspace(head_workspace_bytes(OP_HEAD_BACKWARD, m, rows, cols), dev, workspace,
-                         stream)
-    head = (h.data_ptr(), m, cols, ldh, packed.data_ptr(), bits, rows, scales.data_ptr(),
-            zeros.data_ptr(), groupsize, index.data_ptr())
-    tail = (lse.data_ptr(), zk.data_ptr(), dloss.data_ptr(), out.data_ptr(), lddh,
-            ws.data_ptr() if ws is not None else None, wsb, _stream_ptr(stream, dev))
-    with torch.cuda.device(dev):
-        if logits is None:
-            st, name = lib.gptq_head_loss_backward(*head, *tail), "gptq_head_loss_backward"
-        else:
-            st = lib.gptq_head_distill_backward(*head, logits.data_ptr(), top, temperature, *tail)
-            name = "gptq_head_distill_backward"
-    _check(st, name)
+    m, ldh, dev = _input(h, cols, "h")
+    rows, groupsize = _layer(packed, bits, cols, scales, zeros, groupsize, dev)
+    shape = _head_entries(index, logits, m, dev)
+    _exactly(lse, (m,), _f32, dev, "lse")
+    _exactly(zk, shape, _f32, dev, "the entries' logits")
+    _exactly(dloss, (m,), _f32, dev, "dloss")
+    out, lddh = _out_rows(out, m, cols, _f16, dev)
+    _launch(fn, (h.data_ptr(), m, cols, ldh, packed.data_ptr(), bits, rows, scales.data_ptr(),
+                 zeros.data_ptr(), groupsize, index.data_ptr(), *more, lse.data_ptr(),
+                 zk.data_ptr(), dloss.data_ptr(), out.data_ptr(), lddh),
+            head_workspace_bytes(OP_HEAD_BACKWARD, m, rows, cols), dev, workspace, stream)
     return out
 
 
@@ -748,14 +752,15 @@ def head_loss(h, packed, bits: int, cols: int, scales, zeros, groupsize: int, ta
     (m x cols fp16) and labels target (m int32; outside [0, rows): the token
     takes no part). lse and target_logit are what head_loss_backward takes
     (gptq_head_loss)."""
-    return _head_forward(h, (packed, bits, cols, scales, zeros, groupsize), target, None, 1.0, loss,
-                         lse, target_logit, workspace, stream)
+    return _head_forward(lib.gptq_head_loss, h, (packed, bits, cols, scales, zeros, groupsize),
+                         target, None, (), loss, lse, target_logit, workspace, stream)
 
 
 def head_loss_backward(h, packed, bits: int, cols: int, scales, zeros, groupsize: int, target, lse,
                        target_logit, dloss, out=None, workspace=None, stream=None):
     """dh (m x cols fp16) of sum_t dloss[t] * loss[t] (gptq_head_loss_backward)."""
-    return _head_backward(h, (packed, bits, cols, scales, zeros, groupsize), target, None, 1.0, lse,
+    return _head_backward(lib.gptq_head_loss_backward, h,
+                          (packed, bits, cols, scales, zeros, groupsize), target, None, (), lse,
                           target_logit, dloss, out, workspace, stream)
 
 
@@ -767,10 +772,11 @@ def head_distill(h, packed, bits: int, cols: int, scales, zeros, groupsize: int,
     top_index (int32) and top_logits (fp32), m x top; an index outside
     [0, rows) or a logit of -inf marks an entry that is not there
     (gptq_head_distill)."""
-    if not (temperature > 0 and 1e-30 < temperature < 1e30):
-        raise ValueError("temperature must be positive")
-    return _head_forward(h, (packed, bits, cols, scales, zeros, groupsize), top_index, top_logits,
-                         float(temperature), loss, lse, student_logits, workspace, stream)
+    t = _temperature(temperature)
+    return _head_forward(lib.gptq_head_distill, h, (packed, bits, cols, scales, zeros, groupsize),
+                         top_index, top_logits,
+                         (top_logits.data_ptr(), top_logits.shape[-1], t), loss, lse,
+                         student_logits, workspace, stream)
 
 
 def head_distill_backward(h, packed, bits: int, cols: int, scales, zeros, groupsize: int,
@@ -778,7 +784,8 @@ def head_distill_backward(h, packed, bits: int, cols: int, scales, zeros, groups
                           workspace=None, stream=None):
     """dh (m x cols fp16) of sum_t dloss[t] * loss[t] of head_distill
     (gptq_head_distill_backward)."""
-    if not (temperature > 0 and 1e-30 < temperature < 1e30):
-        raise ValueError("temperature must be positive")
-    return _head_backward(h, (packed, bits, cols, scales, zeros, groupsize), top_index, top_logits,
-                          float(temperature), lse, student_logits, dloss, out, workspace, stream)
+    t = _temperature(temperature)
+    return _head_backward(lib.gptq_head_distill_backward, h,
+                          (packed, bits, cols, scales, zeros, groupsize), top_index, top_logits,
+                          (top_logits.data_ptr(), top_logits.shape[-1], t), lse, student_logits,
+                          dloss, out, workspace, stream)

@@ -148,4 +148,4 @@ def test_python_checks_come_before_the_library():
     with pytest.raises(ValueError, match="h must be"):
         gq.head_loss(x, None, 4, 128, None, None, 128, None)
     with pytest.raises(ValueError, match="temperature"):
-        gq.head_distill(x, None, 4, 128, None, None, 128, None, None, temperature=0.0)
+        gq.head_distill(x, None, 4, 128, None, None, 128, None, x, temperature=0.0)
