@@ -441,8 +441,8 @@ gptq_status gptq_hessian_accumulate_noalloc(float* H, int64_t d, const void* X, 
  *            after another).
  *   count    >= 1, at most 2^20 (gradients: 4096, else GPTQ_ERR_UNSUPPORTED)
  *   rank     >= 1, at most 128 (else GPTQ_ERR_UNSUPPORTED)
- * A[a] x_t and everything after it is fp32; an infinity or NaN in one adapter
- * reaches only its own tokens.
+ * A[a] x_t is fp32; an infinity or NaN in one adapter reaches only its own
+ * tokens.
  */
 typedef struct gptq_adapters {
   const void* A;
@@ -477,10 +477,12 @@ gptq_status gptq_dequant_gemm_adapters(const void* x, int64_t m, int64_t cols, i
 /*
  * gptq_linear_forward_adapters -- gptq_linear_forward (many tokens, fp16 y;
  * the same shapes, alignment and errors) with the tokens' adapters:
- * y = act(x W_hat^T + adapters), the layer's part with
- * gptq_linear_forward's bound, the adapter's with that above, their fp32 sum
- * rounded to fp16.  The groups' sums may
- * be added in another order than gptq_linear_forward adds them.
+ * y = act(x W_hat^T + adapters).  The layer's part is within
+ * (cols + 2 ngroups + 2) * 2^-24 * sum_c |x_c| |code_c - zero| scale (the sums
+ * may be kept in units of the current group's scale, and added in another
+ * order than gptq_linear_forward adds them).  The adapter's part is as above,
+ * with A x held to 2^-23 of the largest of 16 of its values.  Their fp32 sum
+ * is rounded to fp16 once.
  *   Asynchronous; bitwise deterministic.
  */
 gptq_status gptq_linear_forward_adapters(const void* x, int64_t m, int64_t cols, int64_t ldx,
@@ -513,9 +515,10 @@ gptq_status gptq_linear_forward_adapters(const void* x, int64_t m, int64_t cols,
  *              without tokens (all of them when m = 0).
  *   Arithmetic: for dx W_hat is rounded to fp16 (2^-11 relative, 2^-25 below
  *   2^-14; values beyond 65504 become infinite), products are exact in fp32
- *   and summed there, and dx is rounded to fp16 once.  The adapters' parts
- *   are fp32 throughout; their sums run over an adapter's tokens in token
- *   order, 256 at a time, so results are bitwise reproducible.
+ *   and summed there, dv enters it held to 2^-23 of the largest of 16 of its
+ *   values, and dx is rounded to fp16 once.  dA and dB are fp32 throughout;
+ *   their sums run over an adapter's tokens in token order, 256 at a time, so
+ *   results are bitwise reproducible.
  *   Asynchronous.
  */
 gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_t lddy,
@@ -556,8 +559,8 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
  *   dloss        m fp32: the weight of each token's loss (1 / tokens, times
  *                a loss scale that keeps dh inside fp16).
  *   dh           m x cols fp16 out, row t at dh + t*lddh.
- *   Arithmetic: z is formed as gptq_linear_forward forms its sums, without a
- *   rounding to fp16; exp, log and their sums are fp32.  For dh, the
+ *   Arithmetic: z is formed as gptq_linear_forward_adapters forms the layer's
+ *   part, without a rounding to fp16; exp, log and their sums are fp32.  For dh, the
  *   probabilities (p - target in fp32 first) and W_hat are rounded to fp16
  *   (2^-11 relative, 2^-25 below 2^-14), products and sums are fp32, and dh
  *   is rounded to fp16 once.

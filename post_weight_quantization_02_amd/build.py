@@ -14,7 +14,7 @@ BUILD = os.path.join(HERE, "_build")
 
 SOURCES = ["gptq_abi.cpp", "syrk_f16.hip", "chol_f64.hip", "sweep.hip", "act_order.hip", "infer.hip",
            "linear_mfma.hip", "accumulate_noalloc.hip", "adapters.hip", "gemm_f16.hip", "head.hip",
-           "decode_adapters.hip", "train_abi.cpp"]
+           "decode_adapters.hip", "linear_wide.hip", "train_abi.cpp"]
 
 # Per-file code generation options.  The fp64 kernels keep their MFMA
 # accumulators in ordinary VGPRs: with the default AGPR form the compiler

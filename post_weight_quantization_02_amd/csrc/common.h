@@ -175,6 +175,12 @@ hipError_t launch_linear_forward_adapters(int bits, const _Float16* x, int64_t l
 // splits of the input columns when the tiles leave CUs idle (1: none); their
 // fp32 sums, splits x m x rows, go to the workspace
 int linear_splits(int bits, int64_t m, int64_t rows, int64_t cols, int groupsize);
+// whether the tiles are the wide ones, and the floats of workspace that those
+// need for a copy of the scales and zeros (at most: groups of 128)
+bool linear_wide(int bits, int64_t m, int64_t rows);
+int64_t linear_scales(int bits, int64_t m, int64_t rows, int64_t cols);
+hipError_t launch_scales(const float* scales, const float* zeros, int64_t rows, int64_t ngroups,
+                         float* scales_t, float* zeros_t, int64_t pitch, hipStream_t s);
 // the transposed weights, cols x kp (kp >= rows a multiple of kKPad, zeros
 // behind the rows) with row pitch ldt, and the products with them
 constexpr int kKPad = 64;  // K of the fp16 product, padded with zeros
@@ -184,6 +190,9 @@ struct PrepareAdapters {  // what the adapters' gradients need beside them
   int rank;
   int64_t ldb;      // Bt: count x rank x ldb, zeros behind the rows
   _Float16* bt;
+  const _Float16* A;
+  int lda;          // At: count x cols x lda, zeros behind the rank
+  _Float16* at;
   const int* index;
   int64_t m;
   int* list;
@@ -224,12 +233,14 @@ int64_t head_tiles(int bits, int64_t m, int64_t rows);
 hipError_t launch_head_partials(int bits, const _Float16* x, int64_t ldx, int64_t m,
                                 const uint32_t* packed, int64_t rows, int64_t cols,
                                 const float* scales, const float* zeros, int groupsize,
-                                const HeadTargets& tg, float2* part, float* zk, hipStream_t s);
+                                const HeadTargets& tg, float2* part, float* scales_t, float* zk,
+                                hipStream_t s);
 // P[t][r] = exp(z - lse[t]) in fp16, 0 where lse[t] is +inf and for rows <= r < ldp
 hipError_t launch_head_probs(int bits, const _Float16* x, int64_t ldx, int64_t m,
                              const uint32_t* packed, int64_t rows, int64_t cols,
                              const float* scales, const float* zeros, int groupsize, float inv_t,
-                             const float* lse, _Float16* P, int64_t ldp, hipStream_t s);
+                             const float* lse, float* scales_t, _Float16* P, int64_t ldp,
+                             hipStream_t s);
 // lse and the loss from the tiles' partials and the named logits (zk: 0 where
 // an entry takes no part)
 hipError_t launch_head_finish(int64_t m, int64_t rows, const HeadTargets& tg, const float2* part,

@@ -10,35 +10,6 @@ namespace {
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 
-// sum_j v[t][j] up[a][r][j] of one token and output, 0 without an adapter.
-// VEC: rank % 8 == 0 and up 16-byte aligned.
-template <bool VEC>
-__device__ inline float low_rank(const AdapterTile& ad, int64_t t, int64_t r) {
-  const int a = ad.index[t];
-  if (a < 0 || a >= ad.count) return 0.f;
-  const _Float16* up = ad.up + a * ad.stride + r * ad.ns;
-  const float* v = ad.v + t * ad.ldv;
-  float sum = 0.f;
-  if (VEC) {
-    for (int j = 0; j < ad.rank; j += 8) {
-      const half8 u = *reinterpret_cast<const half8*>(up + j);
-      const float4 v0 = *reinterpret_cast<const float4*>(v + j);
-      const float4 v1 = *reinterpret_cast<const float4*>(v + j + 4);
-      sum = __builtin_fmaf(v0.x, (float)u[0], sum);
-      sum = __builtin_fmaf(v0.y, (float)u[1], sum);
-      sum = __builtin_fmaf(v0.z, (float)u[2], sum);
-      sum = __builtin_fmaf(v0.w, (float)u[3], sum);
-      sum = __builtin_fmaf(v1.x, (float)u[4], sum);
-      sum = __builtin_fmaf(v1.y, (float)u[5], sum);
-      sum = __builtin_fmaf(v1.z, (float)u[6], sum);
-      sum = __builtin_fmaf(v1.w, (float)u[7], sum);
-    }
-  } else {
-    for (int j = 0; j < ad.rank; ++j) sum = __builtin_fmaf(v[j], (float)up[j], sum);
-  }
-  return sum;
-}
-
 // ------------------------------------------------------------- MFMA, 4 and 8 bits
 // 16 TT tokens x 16 BT outputs per workgroup; its eight waves take every
 // eighth chunk of 128 columns (so together 1024 adjacent columns of each row
@@ -112,7 +83,7 @@ __device__ inline void transpose_groups(uint32_t (&w)[4]) {
   }
 }
 
-template <int BITS, int TT, int BT, bool VEC>
+template <int BITS, int TT, int BT>
 __global__ __launch_bounds__(64 * kWaves, 2) void decode_mfma_kernel(
     const _Float16* __restrict__ xp, int m, const uint32_t* __restrict__ packed, int64_t nw,
     int64_t rows, int64_t cols, const float* __restrict__ scales,
@@ -181,12 +152,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void decode_mfma_kernel(
   fetch_x(0, cb);
   fetch_x(1, cb + 1);
   // this thread's outputs' low-rank part, its loads beside the first chunks'
+  const bool vec = vec_up(ad);
   float low[PER];
 #pragma unroll
   for (int u = 0; u < PER; ++u) {
     const int o = tid + 64 * kWaves * u, tok = o / (16 * BT);
     const int64_t r = r0 + o % (16 * BT);
-    low[u] = (o < OUT && tok < m && r < rows) ? low_rank<VEC>(ad, tok, r) : 0.f;
+    low[u] = (o < OUT && tok < m && r < rows) ? low_rank(ad, tok, r, vec) : 0.f;
   }
   const half8 ones = {(_Float16)1.f, (_Float16)1.f, (_Float16)1.f, (_Float16)1.f,
                       (_Float16)1.f, (_Float16)1.f, (_Float16)1.f, (_Float16)1.f};
@@ -364,16 +336,11 @@ struct DecodeCall {
 
 template <int BITS, int TT, int BT>
 void decode_mfma(const DecodeCall& c, const AdapterTile& ad, int64_t t0, int mt, hipStream_t s) {
-  const bool vec = ad.rank % 8 == 0 && (reinterpret_cast<uintptr_t>(ad.up) & 15) == 0;
-  const dim3 grid((unsigned)ceil_div(c.rows, 16 * BT));
-#define GPTQ_DECODE(V)                                                                           \
-  hipLaunchKernelGGL((decode_mfma_kernel<BITS, TT, BT, V>), grid, dim3(64 * kWaves), 0, s,       \
-                     c.xp + t0 * c.cols, mt, c.packed, packed_words(c.cols, BITS), c.rows,       \
-                     c.cols, c.scales, c.zeros, ceil_div(c.cols, c.groupsize), c.groupsize,      \
-                     c.y + t0 * c.ldy, c.ldy, from_token(ad, t0))
-  if (vec) GPTQ_DECODE(true);
-  else GPTQ_DECODE(false);
-#undef GPTQ_DECODE
+  hipLaunchKernelGGL((decode_mfma_kernel<BITS, TT, BT>), dim3((unsigned)ceil_div(c.rows, 16 * BT)),
+                     dim3(64 * kWaves), 0, s, c.xp + t0 * c.cols, mt, c.packed,
+                     packed_words(c.cols, BITS), c.rows, c.cols, c.scales, c.zeros,
+                     ceil_div(c.cols, c.groupsize), c.groupsize, c.y + t0 * c.ldy, c.ldy,
+                     from_token(ad, t0));
 }
 
 template <int BITS>

@@ -13,7 +13,7 @@ namespace {
 
 // ------------------------------------------------------- what goes before
 // One launch writes the transposed weights and, for the adapters' gradients,
-// the transposed B and the tokens grouped by adapter: workgroups of one kind
+// A and B the other way round and the tokens grouped by adapter: workgroups of one kind
 // after another, the grouping (a few long ones) first.
 struct Prepare {
   // the layer
@@ -32,13 +32,16 @@ struct Prepare {
   int rank;
   int64_t ldb;
   _Float16* bt;
+  const _Float16* A;
+  int lda;
+  _Float16* at;
   const int* index;
   int64_t m;
   int max_chunks;
   int* list;
   GradChunk* chunks;
   int2* ranges;
-  int64_t bt_blocks, wt_x, wt_blocks;  // workgroups of each kind (wt_x per row of them)
+  int64_t bt_blocks, at_blocks, wt_x, wt_blocks;  // workgroups of each kind (wt_x per row of them)
 };
 
 // 4 and 8 bits, every word inside a group.  A lane takes one word of eight
@@ -121,6 +124,21 @@ __device__ inline void transpose_up(const Prepare& p, int64_t bid) {
   for (int j = 0; j < p.rank; ++j)
     p.bt[(a * p.rank + j) * p.ldb + n] =
         n < p.rows ? p.B[(a * p.rows + n) * p.rank + j] : (_Float16)0.f;
+}
+
+// A_a (rank x cols) -> cols x lda, zeros behind the rank: what add_adapters
+// reads.
+__device__ inline void transpose_down(const Prepare& p, int64_t bid) {
+  const int64_t per = ceil_div(p.cols, 256);
+  const int64_t a = bid / per, c = (bid % per) * 256 + threadIdx.x;
+  if (c >= p.cols) return;
+  for (int j0 = 0; j0 < p.lda; j0 += 8) {
+    half8 v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = j0 + e < p.rank ? p.A[(a * p.rank + j0 + e) * p.cols + c] : (_Float16)0.f;
+    *reinterpret_cast<half8*>(p.at + (a * p.cols + c) * p.lda + j0) = v;
+  }
 }
 
 // Tokens grouped by adapter, in token order inside each (so the gradients'
@@ -211,6 +229,8 @@ __global__ __launch_bounds__(256) void prepare_kernel(Prepare p) {
   bid -= p.count;
   if (bid < p.bt_blocks) return transpose_up(p, bid);
   bid -= p.bt_blocks;
+  if (bid < p.at_blocks) return transpose_down(p, bid);
+  bid -= p.at_blocks;
   if constexpr (WORDS > 0) transpose_words<WORDS>(p, bid % p.wt_x, bid / p.wt_x);
   else transpose_tile(p, bid % p.wt_x, bid / p.wt_x, sh.tile);
 }
@@ -389,17 +409,7 @@ __global__ __launch_bounds__(256) void gemm_reduce_kernel(int splits, int64_t m,
   float v = 0.f;
 #pragma unroll 8
   for (int k = 0; k < splits; ++k) v += o.sums[(k * m + t) * n + c];
-  if constexpr (MODE == kStoreAdapters) {
-    const int a = o.ad.index[t];
-    if (a >= 0 && a < o.ad.count) {
-      const _Float16* up = o.ad.up + a * o.ad.stride + c * o.ad.ns;
-      float low = 0.f;
-#pragma unroll 8
-      for (int j = 0; j < o.ad.rank; ++j)
-        low = __builtin_fmaf(o.ad.v[t * o.ad.ldv + j], (float)up[j * o.ad.js], low);
-      v += low;
-    }
-  }
+  if constexpr (MODE == kStoreAdapters) v += low_rank(o.ad, t, c, vec_up(o.ad));
   if constexpr (MODE == kAccumulate || MODE == kFinish)
     if (!o.first) v += o.c32[t * n + c];
   if constexpr (MODE == kAccumulate) o.c32[t * n + c] = v;
@@ -481,6 +491,10 @@ hipError_t launch_prepare(const uint32_t* packed, int bits, int64_t rows, int64_
     p.rank = ad->rank;
     p.ldb = ad->ldb;
     p.bt = ad->bt;
+    p.A = ad->A;
+    p.lda = ad->lda;
+    p.at = ad->at;
+    p.at_blocks = ad->count * ceil_div(cols, 256);
     p.index = ad->index;
     p.m = ad->m;
     p.max_chunks = (int)grad_chunks(ad->m, ad->count);
@@ -493,7 +507,7 @@ hipError_t launch_prepare(const uint32_t* packed, int bits, int64_t rows, int64_
                      (groupsize % (32 / bits) == 0 || groupsize >= cols);
   p.wt_x = kp / 64;
   p.wt_blocks = p.wt_x * (words ? ceil_div(p.nw, 32) : ceil_div(cols, 64));
-  const dim3 grid((unsigned)(p.count + p.bt_blocks + p.wt_blocks));
+  const dim3 grid((unsigned)(p.count + p.bt_blocks + p.at_blocks + p.wt_blocks));
   if (words && bits == 4) hipLaunchKernelGGL(prepare_kernel<4>, grid, dim3(256), 0, s, p);
   else if (words) hipLaunchKernelGGL(prepare_kernel<8>, grid, dim3(256), 0, s, p);
   else hipLaunchKernelGGL(prepare_kernel<0>, grid, dim3(256), 0, s, p);

@@ -173,7 +173,7 @@ __device__ inline float adapter_share(const AdapterTile& ad, int64_t t, int64_t 
   const _Float16* up = ad.up + a * ad.stride + r * ad.ns;
   float sum = 0.f;
   for (int j = lane; j < ad.rank; j += 64)
-    sum = __builtin_fmaf(ad.v[t * ad.ldv + j], (float)up[j * ad.js], sum);
+    sum = __builtin_fmaf(ad.v[t * ad.ldv + j], (float)up[j], sum);
   return sum;
 }
 

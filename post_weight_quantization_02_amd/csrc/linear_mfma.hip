@@ -35,15 +35,13 @@
 //     (4 bits) or two (8 bits) 16-byte pieces of the packed row.
 //   * XCD-aware order: an XCD works on groups of 4 token tiles x all output
 //     tiles, 4 x 8 tiles at a time, so its L2 serves both operands.
-#include "adapters_dev.h"
-#include "tile_grid.h"
+#include "linear_tails.h"
 
 namespace gptq {
 namespace {
 
 constexpr int KG = 128;    // input columns per stage
 constexpr int NSTAGE = 3;
-constexpr int kGroupM = 4;  // token tiles per XCD-local group
 
 // What depends on the code width: a wave's outputs (WTN), the packed bytes of
 // one output row per stage (RB), and the 16-byte pieces per lane per stage
@@ -360,99 +358,6 @@ __device__ inline void stage_step(int k, int nk, const char* cur, char* nxt, con
   }
 }
 
-// What becomes of a tile's sums:
-//   kStore     fp16 outputs, the layer's own product
-//   kAdapters  the adapters' part added first (adapters_dev.h)
-//   kSplit     fp32 sums of one split of the input columns
-//   kPartials  z = sum * inv_t: per token the tile's max and sum exp(z - max),
-//              the pieces of the softmax statistics of a vocabulary whose
-//              logits are not kept, and the logits that the targets name
-//   kProbs     exp(z - lse) in fp16, the softmax of one piece of it
-enum TailMode { kStore = 0, kAdapters = 1, kSplit = 2, kPartials = 3, kProbs = 4 };
-struct Tail {
-  AdapterTile ad;
-  float* sums;       // splits x m x rows
-  float inv_t;
-  float2* part;      // output tiles x m
-  const float* lse;  // m
-  const int* index;  // m x top
-  int top;
-  float* zk;         // m x top
-};
-
-// (max, sum exp(z - max)) of the tile's outputs for each of its tokens: over
-// the wave's outputs in registers and 16-lane shuffles, over the waves through
-// LDS.  Outputs past the matrix count as -inf.
-template <class L>
-__device__ inline void tile_partials(const f32x4 (&acc)[L::AT][L::BT], const Tail& tail,
-                                     float2* red, int64_t t0, int64_t m, int64_t tn, int64_t nw,
-                                     int64_t rows) {
-  constexpr int AT = L::AT, BT = L::BT, TM = L::TM, NWAVE = L::NWAVE;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, kg = lane >> 4;
-#pragma unroll
-  for (int a = 0; a < AT; ++a)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float z[BT], top = -INFINITY;
-#pragma unroll
-      for (int b = 0; b < BT; ++b) {
-        z[b] = nw + 16 * b + li < rows ? acc[a][b][i] * tail.inv_t : -INFINITY;
-        top = fmaxf(top, z[b]);
-      }
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-      const float base = top == -INFINITY ? 0.f : top;
-      float sum = 0.f;
-#pragma unroll
-      for (int b = 0; b < BT; ++b) sum += __expf(z[b] - base);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-      if (li == 0) red[wave * TM + 16 * a + 4 * kg + i] = make_float2(top, sum);
-    }
-  __syncthreads();
-  if (tid < TM && t0 + tid < m) {
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < NWAVE; ++w) top = fmaxf(top, red[w * TM + tid].x);
-    const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < NWAVE; ++w) {
-      const float2 p = red[w * TM + tid];
-      sum += p.y * (p.x == -INFINITY ? 0.f : __expf(p.x - base));
-    }
-    tail.part[tn * m + t0 + tid] = make_float2(top, sum);
-  }
-}
-
-// zk[t][k] = z[t][index[t][k]] for the named outputs inside the tile: 16
-// tokens' sums at a time go through LDS, and every thread looks its share of
-// the 16 x top entries up.
-template <class L>
-__device__ inline void tile_targets(const f32x4 (&acc)[L::AT][L::BT], const Tail& tail, float* zs,
-                                    int64_t t0, int64_t m, int64_t n0, int64_t rows) {
-  constexpr int PITCH = L::TN + 4;  // rows 4 banks apart
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, kg = lane >> 4;
-  const int64_t end = min(n0 + L::TN, rows);
-#pragma unroll
-  for (int a = 0; a < L::AT; ++a) {
-    if (t0 + 16 * a >= m) break;
-    __syncthreads();
-#pragma unroll
-    for (int b = 0; b < L::BT; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        zs[(4 * kg + i) * PITCH + L::WTN * wave + 16 * b + li] = acc[a][b][i];
-    __syncthreads();
-    const int n = (int)min((int64_t)16, m - t0 - 16 * a) * tail.top;
-    const int64_t e0 = (t0 + 16 * a) * tail.top;
-    for (int e = tid; e < n; e += 64 * L::NWAVE) {
-      const int64_t v = tail.index[e0 + e];
-      if (v >= n0 && v < end) tail.zk[e0 + e] = zs[(e / tail.top) * PITCH + (v - n0)] * tail.inv_t;
-    }
-  }
-}
-
 // The weights of one chunk are 64 (128) bytes of every packed row: rows whose
 // pitch is a multiple of 2 KB put them on an eighth of the memory channels,
 // and workgroups that run in step read them all at once.  Where an XCD has
@@ -533,48 +438,12 @@ __global__ __launch_bounds__(64 * W, 1) void linear_kernel(
   }
   fold_group<AT, BT>(acc, part, fsc);  // the last stage always ends a group
 
-  if constexpr (TAIL == kAdapters)
-    add_adapters<AT, BT>(acc, tail.ad, t0, m, n0 + L::WTN * wave, rows);
-  if constexpr (TAIL == kPartials) {
-    static_assert(L::TM * L::NWAVE * 8 <= L::STAGE && 16 * (L::TN + 4) * 4 <= L::STAGE, "LDS");
-    __syncthreads();  // the stages are free
-    tile_partials<L>(acc, tail, reinterpret_cast<float2*>(st0), t0, m, tn, n0 + L::WTN * wave,
-                     rows);
-    tile_targets<L>(acc, tail, reinterpret_cast<float*>(st1), t0, m, n0, rows);
-    return;
-  }
-
-  // lane holds rows 4 * kg + i of each 16 x 16 tile, column li
-#pragma unroll
-  for (int a = 0; a < AT; ++a)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t t = t0 + 16 * a + 4 * kg + i;
-      if (t >= m) continue;
-      if constexpr (TAIL == kProbs) {
-        const float lse = tail.lse[t];
-#pragma unroll
-        for (int b = 0; b < BT; ++b) {
-          const int64_t r = n0 + L::WTN * wave + 16 * b + li;
-          const bool in = r < rows && lse != INFINITY;
-          const float p = in ? __expf(acc[a][b][i] * tail.inv_t - lse) : 0.f;
-          if (r < ldy) y[t * ldy + r] = (_Float16)p;
-        }
-        continue;
-      }
-#pragma unroll
-      for (int b = 0; b < BT; ++b) {
-        const int64_t r = n0 + L::WTN * wave + 16 * b + li;
-        if (r >= rows) continue;
-        float v = acc[a][b][i];
-        if constexpr (TAIL == kSplit) {
-          tail.sums[((int64_t)blockIdx.y * m + t) * rows + r] = v;
-          continue;
-        }
-        if (RELU) v = v > 0.f ? v : 0.f;
-        y[t * ldy + r] = (_Float16)v;
-      }
-    }
+  LinearCall c{};
+  c.m = m;
+  c.rows = rows;
+  c.y = y;
+  c.ldy = ldy;
+  tile_tail<RELU, TAIL, AT, BT, 1, W>(acc, tail, c, t0, n0, tn, 0, wave, st0, st1);
 }
 
 // The splits of a product added in order, the adapters' part, ReLU, fp16.
@@ -586,54 +455,19 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restr
   const int64_t t = blockIdx.x, r = (int64_t)blockIdx.y * 256 + threadIdx.x;
   if (r >= rows) return;
   float v = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int k = 0; k < splits; ++k) v += sums[(k * m + t) * rows + r];
-  const int a = ad.index[t];
-  if (a >= 0 && a < ad.count) {
-    const _Float16* up = ad.up + a * ad.stride + r * ad.ns;
-    float low = 0.f;
-#pragma unroll 4
-    for (int j = 0; j < ad.rank; ++j)
-      low = __builtin_fmaf(ad.v[t * ad.ldv + j], (float)up[j * ad.js], low);
-    v += low;
-  }
+  v += low_rank(ad, t, r, vec_up(ad));
   if (RELU) v = v > 0.f ? v : 0.f;
   y[t * ldy + r] = (_Float16)v;
 }
 
-// An XCD takes 4 token tiles x 8 output tiles at once (32 KB and 16 KB per
-// stage: the split that minimises its misses).  With fewer than 32 token
-// tiles xm falls below 8, so that an XCD still has 4 of them and the weights
-// are read by fewer XCDs.
-template <class L>
-TileGrid tile_grid(int64_t m, int64_t rows, bool store) {
-  TileGrid g;
-  g.ntm = ceil_div(m, L::TM);
-  g.ntn = ceil_div(rows, L::TN);
-  g.xm = kXcds;
-  if (!store)
-    while (g.xm > 1 && g.ntm < g.xm * kGroupM) g.xm /= 2;
-  const int64_t mine = ceil_div(g.ntm, g.xm);
-  g.gm = store || mine > kGroupM ? kGroupM : (int)mine;
-  return g;
-}
+// The layer's own product: every XCD a share of the token tiles.
+TileGrid store_grid(int64_t ntm, int64_t ntn) { return TileGrid{ntm, ntn, kXcds, kGroupM}; }
 
 int64_t linear_blocks(int bits, int64_t m, int64_t rows) {
-  return (bits == 4 ? tile_grid<Lay<4, 8, 8>>(m, rows, true)
-                    : tile_grid<Lay<8, 8, 8>>(m, rows, true))
-      .blocks();
+  return store_grid(ceil_div(m, 128), ceil_div(rows, 8 * (bits == 4 ? 32 : 16))).blocks();
 }
-
-struct LinearCall {
-  const _Float16* x;
-  int64_t ldx, m;
-  const uint32_t* packed;
-  int64_t rows, cols;
-  const float *scales, *zeros;
-  int groupsize;
-  _Float16* y;
-  int64_t ldy;
-};
 
 template <int BITS, bool RELU, int TAIL, int A, int W>
 hipError_t launch_tile(const LinearCall& c, const Tail& tail, int splits, hipStream_t s) {
@@ -641,7 +475,9 @@ hipError_t launch_tile(const LinearCall& c, const Tail& tail, int splits, hipStr
   const int64_t ngroups = ceil_div(c.cols, g);
   const int gk = (int)ceil_div(g, KG);  // chunks per group (a short last group ends at cols)
   const int64_t nw = c.cols * BITS / 32;
-  const TileGrid grid = tile_grid<Lay<BITS, A, W>>(c.m, c.rows, TAIL == kStore);
+  using L = Lay<BITS, A, W>;
+  const int64_t ntm = ceil_div(c.m, L::TM), ntn = ceil_div(c.rows, L::TN);
+  const TileGrid grid = TAIL == kStore ? store_grid(ntm, ntn) : linear_grid(ntm, ntn);
   hipLaunchKernelGGL((linear_kernel<BITS, RELU, TAIL, A, W>),
                      dim3((unsigned)grid.blocks(), (unsigned)splits), dim3(64 * W), 0, s, c.x,
                      c.ldx, c.m, c.packed, nw, c.rows, c.cols, c.scales, c.zeros, ngroups, gk, grid,
@@ -649,24 +485,56 @@ hipError_t launch_tile(const LinearCall& c, const Tail& tail, int splits, hipStr
   return hipGetLastError();
 }
 
-// The tile by the tokens: 64 tokens x 128 (64) outputs with four waves up to
-// 64 tokens, else 128 x 256 (128).
+// The tile by the tokens and outputs: 64 tokens x 128 (64) outputs with four
+// waves up to 64 tokens; else 128 x 256 (128), or 256 x 256 where that takes
+// less time.  A round of 256 workgroups of the latter takes 1.6 (8 bits: 2.2)
+// times one of the former.
+enum Shape { kFew, kMiddle, kWide };
+Shape shape_of(int bits, int64_t m, int64_t rows) {
+  if (m <= 64) return kFew;
+  const int64_t middle = ceil_div(m, 128) * ceil_div(rows, bits == 4 ? 256 : 128);
+  const int64_t wide = ceil_div(m, 256) * ceil_div(rows, 256);
+  const int cost = bits == 4 ? 16 : 22;
+  return 10 * ceil_div(middle, 256) >= cost * ceil_div(wide, 256) ? kWide : kMiddle;
+}
+
 template <bool RELU, int TAIL>
 hipError_t launch_tail(int bits, const LinearCall& c, const Tail& tail, int splits,
                        hipStream_t s) {
-  if (c.m <= 64)
+  const Shape shape = shape_of(bits, c.m, c.rows);
+  if (shape == kFew)
     return bits == 4 ? launch_tile<4, RELU, TAIL, 4, 4>(c, tail, splits, s)
                      : launch_tile<8, RELU, TAIL, 4, 4>(c, tail, splits, s);
+  if constexpr (TAIL != kSplit)
+    if (shape == kWide) return launch_linear_wide<RELU, TAIL>(bits, c, tail, s);
   return bits == 4 ? launch_tile<4, RELU, TAIL, 8, 8>(c, tail, splits, s)
                    : launch_tile<8, RELU, TAIL, 8, 8>(c, tail, splits, s);
 }
 
-int64_t tail_outputs(int bits, int64_t m) {  // outputs per tile
-  const int waves = m <= 64 ? 4 : 8;
-  return waves * (bits == 4 ? Geo<4>::WTN : Geo<8>::WTN);
+int64_t tail_outputs(int bits, int64_t m, int64_t rows) {  // outputs per tile
+  switch (shape_of(bits, m, rows)) {
+    case kFew: return 4 * (bits == 4 ? Geo<4>::WTN : Geo<8>::WTN);
+    case kMiddle: return 8 * (bits == 4 ? Geo<4>::WTN : Geo<8>::WTN);
+    default: return 256;
+  }
+}
+
+// The scales and zeros as the wide shape reads them.
+hipError_t copy_scales(LinearCall& c, float* to, hipStream_t s) {
+  const int64_t ng = c.groupsize >= c.cols ? 1 : ceil_div(c.cols, c.groupsize);
+  c.pitch_t = round_up(c.rows, 64);
+  c.scales_t = to;
+  c.zeros_t = to + ng * c.pitch_t;
+  return launch_scales(c.scales, c.zeros, c.rows, ng, to, to + ng * c.pitch_t, c.pitch_t, s);
 }
 
 }  // namespace
+
+bool linear_wide(int bits, int64_t m, int64_t rows) { return shape_of(bits, m, rows) == kWide; }
+
+int64_t linear_scales(int bits, int64_t m, int64_t rows, int64_t cols) {
+  return linear_wide(bits, m, rows) ? 2 * ceil_div(cols, KG) * round_up(rows, 64) : 0;
+}
 
 bool linear_forward_supported(int bits, int64_t m, int64_t rows, int64_t cols, int groupsize,
                               const void* x, int64_t ldx, const void* packed) {
@@ -683,7 +551,8 @@ hipError_t launch_linear_forward(int bits, const _Float16* x, int64_t ldx, int64
                                  const uint32_t* packed, int64_t rows, int64_t cols,
                                  const float* scales, const float* zeros, int groupsize, bool relu,
                                  _Float16* y, int64_t ldy, hipStream_t s) {
-  const LinearCall c{x, ldx, m, packed, rows, cols, scales, zeros, groupsize, y, ldy};
+  const LinearCall c{x, ldx, m, packed, rows, cols, scales, zeros, groupsize, y, ldy,
+                     nullptr, nullptr, 0};
   const Tail t{};
   if (bits == 4)
     return relu ? launch_tile<4, true, kStore, 8, 8>(c, t, 1, s)
@@ -693,7 +562,9 @@ hipError_t launch_linear_forward(int bits, const _Float16* x, int64_t ldx, int64
 }
 
 int linear_splits(int bits, int64_t m, int64_t rows, int64_t cols, int groupsize) {
-  const int64_t tiles = ceil_div(m, m <= 64 ? 64 : 128) * ceil_div(rows, tail_outputs(bits, m));
+  if (shape_of(bits, m, rows) == kWide) return 1;
+  const int64_t tiles =
+      ceil_div(m, m <= 64 ? 64 : 128) * ceil_div(rows, tail_outputs(bits, m, rows));
   const int64_t groups = groupsize >= cols ? 1 : ceil_div(cols, groupsize);
   int64_t s = 256 / tiles;
   if (s > cols / KG / 2) s = cols / KG / 2;
@@ -706,7 +577,11 @@ hipError_t launch_linear_forward_adapters(int bits, const _Float16* x, int64_t l
                                           const float* scales, const float* zeros, int groupsize,
                                           bool relu, const AdapterTile& ad, float* sums,
                                           _Float16* y, int64_t ldy, hipStream_t s) {
-  const LinearCall c{x, ldx, m, packed, rows, cols, scales, zeros, groupsize, y, ldy};
+  LinearCall c{x, ldx, m, packed, rows, cols, scales, zeros, groupsize, y, ldy, nullptr, nullptr, 0};
+  if (linear_wide(bits, m, rows)) {
+    const hipError_t e = copy_scales(c, sums, s);
+    if (e != hipSuccess) return e;
+  }
   Tail t{};
   t.ad = ad;
   const int splits = linear_splits(bits, m, rows, cols, groupsize);
@@ -727,14 +602,20 @@ hipError_t launch_linear_forward_adapters(int bits, const _Float16* x, int64_t l
 }
 
 int64_t head_tiles(int bits, int64_t m, int64_t rows) {
-  return ceil_div(rows, tail_outputs(bits, m));
+  return ceil_div(rows, tail_outputs(bits, m, rows));
 }
 
 hipError_t launch_head_partials(int bits, const _Float16* x, int64_t ldx, int64_t m,
                                 const uint32_t* packed, int64_t rows, int64_t cols,
                                 const float* scales, const float* zeros, int groupsize,
-                                const HeadTargets& tg, float2* part, float* zk, hipStream_t s) {
-  const LinearCall c{x, ldx, m, packed, rows, cols, scales, zeros, groupsize, nullptr, 0};
+                                const HeadTargets& tg, float2* part, float* scales_t, float* zk,
+                                hipStream_t s) {
+  LinearCall c{x, ldx, m, packed, rows, cols, scales, zeros, groupsize, nullptr, 0, nullptr,
+               nullptr, 0};
+  if (linear_wide(bits, m, rows)) {
+    const hipError_t e = copy_scales(c, scales_t, s);
+    if (e != hipSuccess) return e;
+  }
   Tail t{};
   t.inv_t = tg.inv_t;
   t.part = part;
@@ -747,8 +628,13 @@ hipError_t launch_head_partials(int bits, const _Float16* x, int64_t ldx, int64_
 hipError_t launch_head_probs(int bits, const _Float16* x, int64_t ldx, int64_t m,
                              const uint32_t* packed, int64_t rows, int64_t cols,
                              const float* scales, const float* zeros, int groupsize, float inv_t,
-                             const float* lse, _Float16* P, int64_t ldp, hipStream_t s) {
-  const LinearCall c{x, ldx, m, packed, rows, cols, scales, zeros, groupsize, P, ldp};
+                             const float* lse, float* scales_t, _Float16* P, int64_t ldp,
+                             hipStream_t s) {
+  LinearCall c{x, ldx, m, packed, rows, cols, scales, zeros, groupsize, P, ldp, nullptr, nullptr, 0};
+  if (linear_wide(bits, m, rows)) {
+    const hipError_t e = copy_scales(c, scales_t, s);
+    if (e != hipSuccess) return e;
+  }
   Tail t{};
   t.inv_t = inv_t;
   t.lse = lse;

@@ -1,0 +1,194 @@
+// The layer's product from its stored form and what the calls do with its sums
+// (linear_mfma.hip, linear_wide.hip).
+#pragma once
+
+#include "adapters_dev.h"
+#include "tile_grid.h"
+
+namespace gptq {
+
+// What becomes of a tile's sums:
+//   kStore     fp16 outputs, the layer's own product
+//   kAdapters  the adapters' part added first (adapters_dev.h)
+//   kSplit     fp32 sums of one split of the input columns
+//   kPartials  z = sum * inv_t: per token the tile's max and sum exp(z - max),
+//              the pieces of the softmax statistics of a vocabulary whose
+//              logits are not kept, and the logits that the targets name
+//   kProbs     exp(z - lse) in fp16, the softmax of one piece of it
+enum TailMode { kStore = 0, kAdapters = 1, kSplit = 2, kPartials = 3, kProbs = 4 };
+struct Tail {
+  AdapterTile ad;
+  float* sums;       // splits x m x rows
+  float inv_t;
+  float2* part;      // output tiles x m
+  const float* lse;  // m
+  const int* index;  // m x top
+  int top;
+  float* zk;         // m x top
+};
+
+// One product: y = x W_hat^T for m tokens.
+struct LinearCall {
+  const _Float16* x;
+  int64_t ldx, m;
+  const uint32_t* packed;
+  int64_t rows, cols;
+  const float *scales, *zeros;
+  int groupsize;
+  _Float16* y;
+  int64_t ldy;
+  const float *scales_t, *zeros_t;  // groups x pitch_t (launch_scales), for the wide shape
+  int64_t pitch_t;
+};
+
+template <bool RELU, int TAIL>
+hipError_t launch_linear_wide(int bits, const LinearCall& c, const Tail& tail, hipStream_t s);
+
+// An XCD takes 4 token tiles x 8 output tiles at once (at 128 x 256 outputs,
+// 32 KB and 16 KB per stage: the split that minimises its misses).  With fewer
+// than 32 token tiles xm falls below 8, so that an XCD still has 4 of them and
+// the weights are read by fewer XCDs.
+constexpr int kGroupM = 4;
+inline TileGrid linear_grid(int64_t ntm, int64_t ntn) {
+  TileGrid g{ntm, ntn, kXcds, kGroupM};
+  while (g.xm > 1 && ntm < g.xm * kGroupM) g.xm /= 2;
+  const int64_t mine = ceil_div(ntm, g.xm);
+  if (mine < g.gm) g.gm = (int)mine;
+  return g;
+}
+
+#ifdef __HIPCC__
+// Below, a workgroup of WM x WN waves holds 16 AT WM tokens x 16 BT WN outputs
+// from (t0, n0) on; this wave is (wm, wn).
+
+// (max, sum exp(z - max)) of the tile's outputs for each of its tokens: over
+// the wave's outputs in registers and 16-lane shuffles, over the waves through
+// LDS.  Outputs past the matrix count as -inf.
+template <int AT, int BT, int WM, int WN>
+__device__ inline void tile_partials(const f32x4 (&acc)[AT][BT], const Tail& tail, float2* red,
+                                     int64_t t0, int64_t m, int64_t tn, int64_t n0, int64_t rows,
+                                     int wm, int wn) {
+  constexpr int TM = 16 * AT * WM;
+  const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, kg = lane >> 4;
+  const int64_t nw = n0 + 16 * BT * wn;
+#pragma unroll
+  for (int a = 0; a < AT; ++a)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float z[BT], top = -INFINITY;
+#pragma unroll
+      for (int b = 0; b < BT; ++b) {
+        z[b] = nw + 16 * b + li < rows ? acc[a][b][i] * tail.inv_t : -INFINITY;
+        top = fmaxf(top, z[b]);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+      const float base = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+#pragma unroll
+      for (int b = 0; b < BT; ++b) sum += __expf(z[b] - base);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+      if (li == 0) red[wn * TM + 16 * (AT * wm + a) + 4 * kg + i] = make_float2(top, sum);
+    }
+  __syncthreads();
+  if (tid < TM && t0 + tid < m) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WN; ++w) top = fmaxf(top, red[w * TM + tid].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < WN; ++w) {
+      const float2 p = red[w * TM + tid];
+      sum += p.y * (p.x == -INFINITY ? 0.f : __expf(p.x - base));
+    }
+    tail.part[tn * m + t0 + tid] = make_float2(top, sum);
+  }
+}
+
+// zk[t][k] = z[t][index[t][k]] for the named outputs inside the tile: 16
+// tokens' sums of every wave row at a time go through LDS, and every thread
+// looks its share of their entries up.
+template <int AT, int BT, int WM, int WN>
+__device__ inline void tile_targets(const f32x4 (&acc)[AT][BT], const Tail& tail, float* zs,
+                                    int64_t t0, int64_t m, int64_t n0, int64_t rows, int wm,
+                                    int wn) {
+  constexpr int TN = 16 * BT * WN, PITCH = TN + 4;  // rows 4 banks apart
+  const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, kg = lane >> 4;
+  const int64_t end = min(n0 + TN, rows);
+#pragma unroll
+  for (int a = 0; a < AT; ++a) {
+    if (t0 + 16 * a >= m) break;
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < BT; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        zs[(16 * wm + 4 * kg + i) * PITCH + 16 * (BT * wn + b) + li] = acc[a][b][i];
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WM; ++w) {
+      const int64_t t = t0 + 16 * (AT * w + a);
+      if (t >= m) break;
+      const int n = (int)min((int64_t)16, m - t) * tail.top;
+      const int64_t e0 = t * tail.top;
+      for (int e = tid; e < n; e += 64 * WM * WN) {
+        const int64_t v = tail.index[e0 + e];
+        if (v >= n0 && v < end)
+          tail.zk[e0 + e] = zs[(16 * w + e / tail.top) * PITCH + (v - n0)] * tail.inv_t;
+      }
+    }
+  }
+}
+
+// s0 and s1: LDS that the product is done with (behind a barrier, taken here).
+template <bool RELU, int TAIL, int AT, int BT, int WM, int WN>
+__device__ inline void tile_tail(f32x4 (&acc)[AT][BT], const Tail& tail, const LinearCall& c,
+                                 int64_t t0, int64_t n0, int64_t tn, int wm, int wn, char* s0,
+                                 char* s1) {
+  const int lane = threadIdx.x & 63, li = lane & 15, kg = lane >> 4;
+  const int64_t tw = t0 + 16 * AT * wm, nw = n0 + 16 * BT * wn, m = c.m, rows = c.rows;
+  if constexpr (TAIL == kAdapters) add_adapters<AT, BT>(acc, tail.ad, tw, m, nw, rows);
+  if constexpr (TAIL == kPartials) {
+    __syncthreads();
+    tile_partials<AT, BT, WM, WN>(acc, tail, reinterpret_cast<float2*>(s0), t0, m, tn, n0, rows, wm,
+                                  wn);
+    tile_targets<AT, BT, WM, WN>(acc, tail, reinterpret_cast<float*>(s1), t0, m, n0, rows, wm, wn);
+    return;
+  }
+  // lane holds rows 4 * kg + i of each 16 x 16 tile, column li
+#pragma unroll
+  for (int a = 0; a < AT; ++a)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = tw + 16 * a + 4 * kg + i;
+      if (t >= m) continue;
+      if constexpr (TAIL == kProbs) {
+        const float lse = tail.lse[t];
+#pragma unroll
+        for (int b = 0; b < BT; ++b) {
+          const int64_t r = nw + 16 * b + li;
+          const bool in = r < rows && lse != INFINITY;
+          const float p = in ? __expf(acc[a][b][i] * tail.inv_t - lse) : 0.f;
+          if (r < c.ldy) c.y[t * c.ldy + r] = (_Float16)p;
+        }
+        continue;
+      }
+#pragma unroll
+      for (int b = 0; b < BT; ++b) {
+        const int64_t r = nw + 16 * b + li;
+        if (r >= rows) continue;
+        float v = acc[a][b][i];
+        if constexpr (TAIL == kSplit) {
+          tail.sums[((int64_t)blockIdx.y * m + t) * rows + r] = v;
+          continue;
+        }
+        if (RELU) v = v > 0.f ? v : 0.f;
+        c.y[t * c.ldy + r] = (_Float16)v;
+      }
+    }
+}
+#endif
+
+}  // namespace gptq

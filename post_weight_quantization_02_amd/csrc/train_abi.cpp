@@ -32,6 +32,12 @@ struct Carve {
   }
 };
 
+int64_t most(int64_t a, int64_t b) { return a > b ? a : b; }
+
+int64_t scales_copy(int64_t m, int64_t rows, int64_t cols) {  // of either number of bits
+  return most(linear_scales(4, m, rows, cols), linear_scales(8, m, rows, cols));
+}
+
 int rank_pitch(int rank) { return (int)round_up(rank, 16); }
 
 // the sums of a split product
@@ -48,7 +54,7 @@ int64_t gemm_pitch(int64_t k) { return k + 128; }
 struct BackwardLayout {
   int64_t kp;   // rows padded to the fp16 product's K
   int64_t ldt;  // pitch of the transposed weights and of dy's copy
-  size_t wt, dyp, sums, v, dv, bt, list, chunks, ranges, part_a, part_b, total;
+  size_t wt, dyp, sums, v, dv, bt, at, list, chunks, ranges, part_a, part_b, total;
 };
 
 BackwardLayout backward_layout(int64_t m, int64_t rows, int64_t cols, int64_t count, int rank) {
@@ -64,6 +70,7 @@ BackwardLayout backward_layout(int64_t m, int64_t rows, int64_t cols, int64_t co
     L.v = c.take(m * rank_pitch(rank), 4);
     L.dv = c.take(m * rank_pitch(rank), 4);
     L.bt = c.take(count * rank * round_up(rows, 8), 2);
+    L.at = c.take(count * cols * rank_pitch(rank), 2);
     L.list = c.take(m, 4);
     L.chunks = c.take(chunks, sizeof(GradChunk));
     L.ranges = c.take(count, sizeof(int2));
@@ -76,7 +83,7 @@ BackwardLayout backward_layout(int64_t m, int64_t rows, int64_t cols, int64_t co
 
 struct HeadLayout {
   int64_t tokens, width, pieces;  // tokens and vocabulary entries per pass, passes over the latter
-  size_t lse, scale, probs, wt, acc, sums, total;
+  size_t lse, scale, probs, wt, acc, sums, scales, total;
 };
 
 // A pass keeps at most 2^25 probabilities (64 MB, which the 256 MB Infinity
@@ -97,20 +104,25 @@ HeadLayout head_layout(int64_t m, int64_t rows, int64_t cols) {
   L.acc = c.take(L.pieces > 1 ? L.tokens * cols : 0, 4);
   // the last pass over the tokens may split more than the others
   const int64_t rest = m % L.tokens;
-  const int64_t most = split_sums(L.tokens, cols, w);
-  const int64_t last = rest > 0 ? split_sums(rest, cols, w) : 0;
-  L.sums = c.take(most > last ? most : last, 4);
+  L.sums = c.take(most(split_sums(L.tokens, cols, w), rest > 0 ? split_sums(rest, cols, w) : 0), 4);
+  // (so may the last piece of the vocabulary have another tile shape)
+  const int64_t tail = rows % w, few = rest > 0 ? rest : L.tokens;
+  int64_t copy = most(scales_copy(L.tokens, w, cols), scales_copy(few, w, cols));
+  if (tail > 0)
+    copy = most(copy, most(scales_copy(L.tokens, tail, cols), scales_copy(few, tail, cols)));
+  L.scales = c.take(copy, 4);
   L.total = c.at;
   return L;
 }
 
 size_t partials_bytes(int64_t m, int64_t rows) {
-  // the 8-bit kernel's smaller tiles: the more of the two
-  return align_up((size_t)(head_tiles(8, m, rows) * m) * sizeof(float2));
+  return align_up((size_t)(most(head_tiles(4, m, rows), head_tiles(8, m, rows)) * m) *
+                  sizeof(float2));
 }
 
-// The tokens' v, then what the product needs beside it: the splits' sums
-// (many tokens), or x in the decode product's order (whole 64-token passes).
+// The tokens' v, then what the product needs beside it: the splits' sums or
+// the scales' copy (many tokens), or x in the decode product's order (whole
+// 64-token passes).
 size_t forward_v_bytes(int64_t m, int rank) {
   return align_up((size_t)m * rank_pitch(rank) * sizeof(float));
 }
@@ -121,7 +133,9 @@ size_t forward_bytes(int64_t m, int64_t rows, int64_t cols, int rank) {
   const int splits = s4 > s8 ? s4 : s8;
   const size_t sums = splits > 1 ? (size_t)splits * m * rows * sizeof(float) : 0;
   const size_t xp = cols % 128 == 0 ? (size_t)round_up(m, 64) * cols * sizeof(_Float16) : 0;
-  return forward_v_bytes(m, rank) + align_up(sums > xp ? sums : xp);
+  const size_t copy = (size_t)scales_copy(m, rows, cols) * sizeof(float);  // with one split only
+  const size_t more = sums > xp ? sums : xp;
+  return forward_v_bytes(m, rank) + align_up(more > copy ? more : copy);
 }
 
 bool sizes_ok(int64_t m, int64_t rows, int64_t cols, int bits, int groupsize) {
@@ -177,7 +191,6 @@ AdapterTile forward_tile(const gptq_adapters* ad, int64_t rows, const float* v) 
   t.index = ad->index;
   t.up = reinterpret_cast<const _Float16*>(ad->B);
   t.stride = rows * ad->rank;
-  t.js = 1;
   t.ns = ad->rank;
   t.rank = ad->rank;
   t.count = (int)ad->count;
@@ -312,11 +325,13 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
     float* v = reinterpret_cast<float*>(ws + L.v);
     float* dv = reinterpret_cast<float*>(ws + L.dv);
     _Float16* bt = reinterpret_cast<_Float16*>(ws + L.bt);
+    _Float16* at = reinterpret_cast<_Float16*>(ws + L.at);
     int* list = reinterpret_cast<int*>(ws + L.list);
     GradChunk* chunks = reinterpret_cast<GradChunk*>(ws + L.chunks);
     int2* ranges = reinterpret_cast<int2*>(ws + L.ranges);
     const int64_t ldt = round_up(rows, 8);
     const PrepareAdapters pa{reinterpret_cast<const _Float16*>(ad->B), count, rank, ldt, bt,
+                             reinterpret_cast<const _Float16*>(ad->A), rank_pitch(rank), at,
                              ad->index, m, list, chunks, ranges};
     GPTQ_TRY(launch_prepare(packed, bits, rows, cols, scales, zeros, groupsize, g_idx, L.kp, L.ldt,
                             wt, &pa, s));
@@ -349,10 +364,9 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
     gb.cs = rank;
     GPTQ_TRY(launch_grads(ga, gb, m, count, rank, rank_pitch(rank), list, chunks, ranges, s));
     tile = forward_tile(ad, rows, dv);
-    tile.up = reinterpret_cast<const _Float16*>(ad->A);
-    tile.stride = rank * cols;
-    tile.js = cols;
-    tile.ns = 1;
+    tile.up = at;
+    tile.stride = cols * rank_pitch(rank);
+    tile.ns = rank_pitch(rank);
   } else {
     GPTQ_TRY(launch_prepare(packed, bits, rows, cols, scales, zeros, groupsize, g_idx, L.kp, L.ldt,
                             wt, nullptr, s));
@@ -366,7 +380,8 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
 size_t gptq_head_workspace_bytes(int op, int64_t m, int64_t rows, int64_t cols) {
   if (m < 1 || m > kMaxTokens || rows < 1 || cols < 1 || rows > kMaxDim || cols > kMaxDim) return 0;
   switch (op) {
-    case GPTQ_OP_HEAD_LOSS: return partials_bytes(m, rows);
+    case GPTQ_OP_HEAD_LOSS:
+      return partials_bytes(m, rows) + align_up((size_t)scales_copy(m, rows, cols) * sizeof(float));
     case GPTQ_OP_HEAD_BACKWARD: return head_layout(m, rows, cols).total;
     default: return 0;
   }
@@ -415,7 +430,10 @@ gptq_status head_forward(const void* h, int64_t m, int64_t cols, int64_t ldh,
   const _Float16* x = reinterpret_cast<const _Float16*>(h);
   float2* part = reinterpret_cast<float2*>(workspace);
   GPTQ_TRY(launch_head_partials(bits, x, ldh, m, packed, rows, cols, scales, zeros, groupsize,
-                                tg, part, zk, s));
+                                tg, part,
+                                reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) +
+                                                         partials_bytes(m, rows)),
+                                zk, s));
   GPTQ_TRY(launch_head_finish(m, rows, tg, part, head_tiles(bits, m, rows), loss, lse, zk, s));
   return GPTQ_OK;
 }
@@ -462,7 +480,8 @@ gptq_status head_backward(const void* h, int64_t m, int64_t cols, int64_t ldh,
       const int64_t wp = round_up(w, kKPad), ld = gemm_pitch(wp);
       const bool last = v0 + w == rows;
       GPTQ_TRY(launch_head_probs(bits, x, ldh, mt, packed + v0 * nw, w, cols, scales + v0 * ng,
-                                 zeros + v0 * ng, groupsize, tg.inv_t, lse_eff + t0, P, ld, s));
+                                 zeros + v0 * ng, groupsize, tg.inv_t, lse_eff + t0,
+                                 reinterpret_cast<float*>(ws + L.scales), P, ld, s));
       GPTQ_TRY(launch_head_scatter(tt, mt, rows, v0, w, zk + t0 * top, lse + t0, P, ld, s));
       GPTQ_TRY(launch_prepare(packed + v0 * nw, bits, w, cols, scales + v0 * ng, zeros + v0 * ng,
                               groupsize, nullptr, wp, ld, wt, nullptr, s));

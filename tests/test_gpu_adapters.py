@@ -7,10 +7,17 @@ matrix instruction sums no less accurately than that):
 
   v = s A x     (cols + 2) u |s| sum |A x|: the products are exact, s once
   low = B v     v's error through |B|, and (rank + 2) u sum |B v|
+  low (fp16)    in the products with fp16 outputs v is two fp16 numbers in units
+                of the largest of 16 of its values: hi rounds to 2^-11, lo to
+                half a step, 2^-25 or less of that unit where it is subnormal
+                (2^-24 of the largest value, which is at least half a unit):
+                2 u of it in all, through |B|; and the same sums as low
   y (decode)    the layer's own bound F u sum |x| (|q| + |z|) s (as for the
                 product without adapters), low's, and one rounding of the sum
-  y (fp16)      (g + ngroups + 2) u sum |x| |q - z| s, low's, 2 u |y|, and half
-                an fp16 step at |y| plus all that
+  y (fp16)      (cols + 2 ngroups + 2) u sum |x| |q - z| s (the sums of many
+                tokens are kept in units of the current group's scale: two
+                roundings a group), low's, 2 u |y|, and half an fp16 step at
+                |y| plus all that
   dx            W_hat rounds to fp16 (2^-11 of it, or 2^-25 below 2^-14; 2 u for
                 its fp32 form), (rows + 2) u sum |dy W|, A^T dv as low, half an
                 fp16 step
@@ -91,6 +98,16 @@ def _low(x, A, B, s, idx):
                                    np.abs(A), np.abs(B), np.abs(s.astype(np.float64)), idx)
 
 
+def _low_halves(x, A, B, s, idx):
+    """2 u times each token's largest possible |v| through sum |B|."""
+    out = np.zeros((len(x), B.shape[1]))
+    for t, a in enumerate(oracle.adapter_of(idx, len(A))):
+        if a >= 0:
+            v = abs(float(s[a])) * (np.abs(A[a].astype(np.float64)) @ np.abs(x[t].astype(np.float64)))
+            out[t] = 2 * U * v.max() * np.abs(B[a].astype(np.float64)).sum(1)
+    return out
+
+
 def _decode_bound(L, x, m):
     k = 32 // L.bits
     nw = -(-L.cols // k)
@@ -155,8 +172,9 @@ def _forward(env, L, m, n, rank, kind, relu, seed):
                                    _cuda(env, s), _cuda(env, idx), relu=relu)
     torch.cuda.synchronize()
     ref = oracle.adapters_forward(x, L.W, A, B, s, idx)
-    tol = (L.gg + L.ng + 2) * U * (np.abs(x.astype(np.float64)) @ np.abs(L.W).T) \
-        + (L.cols + rank + 6) * U * _low(x, A, B, s, idx) + 2 * U * np.abs(ref)
+    tol = (L.cols + 2 * L.ng + 2) * U * (np.abs(x.astype(np.float64)) @ np.abs(L.W).T) \
+        + (L.cols + rank + 6) * U * _low(x, A, B, s, idx) + _low_halves(x, A, B, s, idx) \
+        + 2 * U * np.abs(ref)
     tol += half_step16(np.abs(ref) + tol)
     if relu:
         ref = np.maximum(ref, 0)
@@ -178,9 +196,9 @@ def test_forward_with_adapters(env, m, rows, cols, bits, g, n, rank, kind, relu)
 
 
 def test_tokens_without_adapter_get_the_layers_own_product(env):
-    """Both products may add in another order than without adapters, so they
-    are within the layer's own bound of the exact sum, twice that apart, and
-    the one for many tokens is rounded to fp16 besides: a half step each,
+    """Both products may add in another order than without adapters: each is
+    within its own bound of the exact sum, the sum of the bounds apart, and
+    the ones for many tokens are rounded to fp16 besides: a half step each,
     taken at the larger value."""
     torch, gq = env
     L = Layer(env, 96, 512, 4, 128, 1)
@@ -195,7 +213,7 @@ def test_tokens_without_adapter_get_the_layers_own_product(env):
         if m == 6:
             tol = 2 * _decode_bound(L, x, m)
         else:
-            tol = 2 * (L.gg + L.ng + 2) * U * (np.abs(x) @ np.abs(L.W).T)
+            tol = (L.gg + L.cols + 3 * L.ng + 4) * U * (np.abs(x) @ np.abs(L.W).T)
             tol += 2 * half_step16(np.abs(y0) + tol)
         assert np.all(np.abs(y - y0)[0::2] <= tol[0::2])
         assert (y[1::2] != y0[1::2]).any()
@@ -269,6 +287,7 @@ def _backward(env, L, m, n, rank, kind, seed, dy_scale=0.05):
         low, mA, mB = oracle.adapters_backward(ady, ax, np.zeros_like(L.W), np.abs(A), np.abs(B), s,
                                                idx)
         tol += (L.rows + rank + 6) * U * low + 2 * U * np.abs(ref)
+        tol += _low_halves(dy, B.transpose(0, 2, 1), A.transpose(0, 2, 1), s, idx)
         sums = m + m // 256 + 8
         for got, want, mag, inner in ((dA, rA, mA, L.rows), (dB, rB, mB, L.cols)):
             err = np.abs(got.cpu().numpy() - want)

@@ -3,7 +3,8 @@ the GPU against the fp64 oracle, every output compared; then a training step
 of adapters through a block and the projection.
 
 Bounds (u = 2^-24):
-  z      (g + ngroups + 3) u sum |h| |q - z| s / T, as the layer's product
+  z      (cols + 2 ngroups + 3) u sum |h| |q - z| s / T, as the product with
+         adapters
   exp    off by at most 4 u (|z - lse| + 2) of itself (the argument's rounding
          and the instruction's), so the sum of exponentials by the average of
          that over the softmax, and (40 + tiles / 64) u for its additions
@@ -69,7 +70,7 @@ def _compare(env, L, h, index, logits, T, dloss, got):
     m = len(h)
     rl, rlse, rzk, z = oracle.head_loss(h, L.W, index, logits, T)
     p, part = oracle.head_targets(index, logits, L.rows, T)
-    ez = (L.gg + L.ng + 3) * U * (np.abs(h.astype(np.float64)) @ np.abs(L.W).T) / T
+    ez = (L.cols + 2 * L.ng + 3) * U * (np.abs(h.astype(np.float64)) @ np.abs(L.W).T) / T
     soft = np.exp(z - rlse[:, None])
     tiles = -(-L.rows // 128)
     elog = 4 * U * (np.abs(z - rlse[:, None]) + 2)
