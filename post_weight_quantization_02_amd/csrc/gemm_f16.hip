@@ -6,6 +6,7 @@
 // (at most 2^-11 of its size, 2^-25 below 2^-14); the products are exact in
 // fp32 and summed there.
 #include "adapters_dev.h"
+#include "store_tile.h"
 #include "tile_grid.h"
 
 namespace gptq {
@@ -376,13 +377,35 @@ __global__ __launch_bounds__(512, 1) void gemm_nt_kernel(const _Float16* __restr
 
   const int64_t tw = t0 + 16 * AT * wm, nw = n0 + 16 * BT * wn;  // this wave's corner
   if constexpr (MODE == kStoreAdapters) add_adapters<AT, BT>(acc, o.ad, tw, m, nw, n);
+  if constexpr (MODE == kStore || MODE == kStoreAdapters || MODE == kFinish) {
+    lds_barrier();  // the stages are free: every wave's reads are in its products
+    char* lds = ring + StoreTile<BT>::kBytes * wave;
+    const bool wide = wide_rows(o.c16, o.ldc);
+#pragma unroll
+    for (int a = 0; a < AT; ++a) {
+      if constexpr (MODE == kFinish) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t t = tw + 16 * a + 4 * kg + i;
+          if (t >= m) continue;
+#pragma unroll
+          for (int b = 0; b < BT; ++b) {
+            const int64_t c = nw + 16 * b + li;
+            if (!o.first && c < n) acc[a][b][i] += o.c32[t * n + c];
+            acc[a][b][i] *= o.scale[t];
+          }
+        }
+      }
+      store_rows<BT>(acc[a], lds, o.c16, o.ldc, tw + 16 * a, m, nw, n, wide);
+    }
+    return;
+  }
 #pragma unroll
   for (int a = 0; a < AT; ++a)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t t = tw + 16 * a + 4 * kg + i;
       if (t >= m) continue;
-      const float scale = MODE == kFinish ? o.scale[t] : 1.f;
 #pragma unroll
       for (int b = 0; b < BT; ++b) {
         const int64_t c = nw + 16 * b + li;
@@ -390,12 +413,10 @@ __global__ __launch_bounds__(512, 1) void gemm_nt_kernel(const _Float16* __restr
         float v = acc[a][b][i];
         if constexpr (MODE == kSplit) {
           o.sums[((int64_t)blockIdx.y * m + t) * n + c] = v;
-          continue;
-        }
-        if constexpr (MODE == kAccumulate || MODE == kFinish)
+        } else {
           if (!o.first) v += o.c32[t * n + c];
-        if constexpr (MODE == kAccumulate) o.c32[t * n + c] = v;
-        else o.c16[t * o.ldc + c] = (_Float16)(MODE == kFinish ? scale * v : v);
+          o.c32[t * n + c] = v;
+        }
       }
     }
 }

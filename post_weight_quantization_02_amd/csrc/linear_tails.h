@@ -3,6 +3,7 @@
 #pragma once
 
 #include "adapters_dev.h"
+#include "store_tile.h"
 #include "tile_grid.h"
 
 namespace gptq {
@@ -158,23 +159,42 @@ __device__ inline void tile_tail(f32x4 (&acc)[AT][BT], const Tail& tail, const L
     return;
   }
   // lane holds rows 4 * kg + i of each 16 x 16 tile, column li
+  if constexpr (TAIL == kAdapters || TAIL == kProbs) {
+    static_assert(StoreTile<BT>::kBytes * WM * WN <= 32 * 1024, "LDS of a stage");
+    __syncthreads();  // the stages are free
+    char* lds = s0 + StoreTile<BT>::kBytes * (threadIdx.x >> 6);
+    const bool wide = wide_rows(c.y, c.ldy);
+    // probabilities go on in zeros to the end of the piece's rows
+    const int64_t end = TAIL == kProbs ? min(c.ldy, n0 + 16 * BT * WN) : rows;
+#pragma unroll
+    for (int a = 0; a < AT; ++a) {
+      f32x4 v[BT];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t t = tw + 16 * a + 4 * kg + i;
+        const float lse = TAIL == kProbs && t < m ? tail.lse[t] : 0.f;
+#pragma unroll
+        for (int b = 0; b < BT; ++b) {
+          float x = acc[a][b][i];
+          if constexpr (TAIL == kProbs) {
+            const bool in = nw + 16 * b + li < rows && lse != INFINITY;
+            x = in ? __expf(x * tail.inv_t - lse) : 0.f;
+          } else if (RELU) {
+            x = x > 0.f ? x : 0.f;
+          }
+          v[b][i] = x;
+        }
+      }
+      store_rows<BT>(v, lds, c.y, c.ldy, tw + 16 * a, m, nw, end, wide);
+    }
+    return;
+  }
 #pragma unroll
   for (int a = 0; a < AT; ++a)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t t = tw + 16 * a + 4 * kg + i;
       if (t >= m) continue;
-      if constexpr (TAIL == kProbs) {
-        const float lse = tail.lse[t];
-#pragma unroll
-        for (int b = 0; b < BT; ++b) {
-          const int64_t r = nw + 16 * b + li;
-          const bool in = r < rows && lse != INFINITY;
-          const float p = in ? __expf(acc[a][b][i] * tail.inv_t - lse) : 0.f;
-          if (r < c.ldy) c.y[t * c.ldy + r] = (_Float16)p;
-        }
-        continue;
-      }
 #pragma unroll
       for (int b = 0; b < BT; ++b) {
         const int64_t r = nw + 16 * b + li;
