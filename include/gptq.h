@@ -531,8 +531,8 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
 
 /*
  * Losses through a stored vocabulary projection (rows = vocabulary entries),
- * z = W_hat h.  The logits are never kept: a piece of at most 8192 entries
- * (2^25 probabilities) is in the workspace at a time.
+ * z = W_hat h.  The logits are never kept: a piece of at most 2^25
+ * probabilities (and 2^26 weights) is in the workspace at a time.
  *
  * gptq_head_loss -- softmax cross entropy, loss[t] = lse(z_t) - z_t[y_t]: the
  * training loss, and the score behind a perplexity.
@@ -560,10 +560,12 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
  *                a loss scale that keeps dh inside fp16).
  *   dh           m x cols fp16 out, row t at dh + t*lddh.
  *   Arithmetic: z is formed as gptq_linear_forward_adapters forms the layer's
- *   part, without a rounding to fp16; exp, log and their sums are fp32.  For dh, the
- *   probabilities (p - target in fp32 first) and W_hat are rounded to fp16
- *   (2^-11 relative, 2^-25 below 2^-14), products and sums are fp32, and dh
- *   is rounded to fp16 once.
+ *   part, without a rounding to fp16; exp, log and their sums are
+ *   fp32.  For dh, W_hat and the probabilities are rounded to fp16 (2^-11
+ *   relative, 2^-25 below 2^-14), those of the named entries (p - target, in
+ *   fp32) with what the rounding leaves added again where it is 1/32 of the
+ *   token's largest or more; products and sums are fp32, and dh is rounded to
+ *   fp16 once.
  *   Asynchronous; bitwise deterministic.
  */
 gptq_status gptq_head_loss(const void* h, int64_t m, int64_t cols, int64_t ldh,
@@ -597,8 +599,9 @@ gptq_status gptq_head_distill_backward(const void* h, int64_t m, int64_t cols, i
                                        void* stream);
 
 /* Bytes of workspace of the calls above (op: GPTQ_OP_HEAD_LOSS or
- * GPTQ_OP_HEAD_BACKWARD); 0 for sizes the operation would reject. */
-size_t gptq_head_workspace_bytes(int op, int64_t m, int64_t rows, int64_t cols);
+ * GPTQ_OP_HEAD_BACKWARD; top 1 for labels); 0 for sizes the operation would
+ * reject. */
+size_t gptq_head_workspace_bytes(int op, int64_t m, int64_t rows, int64_t cols, int top);
 
 #ifdef __cplusplus
 }

@@ -98,7 +98,7 @@ _ad = ctypes.POINTER(_Adapters)
 lib.gptq_adapters_workspace_bytes.restype = _sz
 lib.gptq_adapters_workspace_bytes.argtypes = [_int, _i64, _i64, _i64, _i64, _int]
 lib.gptq_head_workspace_bytes.restype = _sz
-lib.gptq_head_workspace_bytes.argtypes = [_int, _i64, _i64, _i64]
+lib.gptq_head_workspace_bytes.argtypes = [_int, _i64, _i64, _i64, _int]
 lib.gptq_dequant_gemm_adapters.restype = _int
 lib.gptq_dequant_gemm_adapters.argtypes = [_p, _i64, _i64, _i64, _p, _int, _i64, _p, _p, _int, _p,
                                            _ad, _p, _i64, _p, _sz, _p]
@@ -515,9 +515,10 @@ def adapters_workspace_bytes(op: int, m: int, rows: int, cols: int, count: int =
 
 
 @functools.lru_cache(maxsize=1024)
-def head_workspace_bytes(op: int, m: int, rows: int, cols: int) -> int:
-    """Workspace of OP_HEAD_LOSS or OP_HEAD_BACKWARD for m tokens."""
-    return int(lib.gptq_head_workspace_bytes(op, m, rows, cols))
+def head_workspace_bytes(op: int, m: int, rows: int, cols: int, top: int = 1) -> int:
+    """Workspace of OP_HEAD_LOSS or OP_HEAD_BACKWARD for m tokens and top
+    entries each (labels: 1)."""
+    return int(lib.gptq_head_workspace_bytes(op, m, rows, cols, top))
 
 
 def _rows_of(t, m, n, dtype, dev, name):
@@ -725,7 +726,7 @@ def _head_forward(fn, h, layer, index, logits, more, loss, lse, zk, workspace, s
     _launch(fn, (h.data_ptr(), m, cols, ldh, packed.data_ptr(), bits, rows, scales.data_ptr(),
                  zeros.data_ptr(), groupsize, index.data_ptr(), *more, loss.data_ptr(),
                  lse.data_ptr(), zk.data_ptr()),
-            head_workspace_bytes(OP_HEAD_LOSS, m, rows, cols), dev, workspace, stream)
+            head_workspace_bytes(OP_HEAD_LOSS, m, rows, cols, shape[-1] if more else 1), dev, workspace, stream)
     return loss, lse, zk
 
 
@@ -741,7 +742,7 @@ def _head_backward(fn, h, layer, index, logits, more, lse, zk, dloss, out, works
     _launch(fn, (h.data_ptr(), m, cols, ldh, packed.data_ptr(), bits, rows, scales.data_ptr(),
                  zeros.data_ptr(), groupsize, index.data_ptr(), *more, lse.data_ptr(),
                  zk.data_ptr(), dloss.data_ptr(), out.data_ptr(), lddh),
-            head_workspace_bytes(OP_HEAD_BACKWARD, m, rows, cols), dev, workspace, stream)
+            head_workspace_bytes(OP_HEAD_BACKWARD, m, rows, cols, shape[-1] if more else 1), dev, workspace, stream)
     return out
 
 

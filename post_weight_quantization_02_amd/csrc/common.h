@@ -210,9 +210,9 @@ hipError_t launch_pad_rows(const _Float16* src, int64_t lds, int64_t m, int64_t 
 hipError_t launch_gemm_nt_f16(const _Float16* A, int64_t lda, int64_t m, const _Float16* B,
                               int64_t ldb, int64_t n, int64_t K, const AdapterTile* ad,
                               float* sums, _Float16* C, int64_t ldc, hipStream_t s);
-// C32 (+)= A B^T, or with C16 the finished rows: C16 = fp16(scale[t] (C32 + A B^T))
+// C32 += A B^T, or with C16 the finished rows: C16 = fp16(scale[t] (C32 + A B^T))
 hipError_t launch_gemm_nt_acc(const _Float16* A, int64_t lda, int64_t m, const _Float16* B,
-                              int64_t ldb, int64_t n, int64_t K, bool first, float* C32,
+                              int64_t ldb, int64_t n, int64_t K, float* C32,
                               const float* scale, float* sums, _Float16* C16, int64_t ldc,
                               hipStream_t s);
 // splits of K when the tiles leave CUs idle (1: none); their fp32 sums,
@@ -245,13 +245,18 @@ hipError_t launch_head_probs(int bits, const _Float16* x, int64_t ldx, int64_t m
 // an entry takes no part)
 hipError_t launch_head_finish(int64_t m, int64_t rows, const HeadTargets& tg, const float2* part,
                               int64_t tiles, float* loss, float* lse, float* zk, hipStream_t s);
-// lse_eff[t] = lse[t] or +inf, gscale[t] = dloss[t] inv_t or 0 (no entries)
-hipError_t launch_head_rows(const HeadTargets& tg, int64_t m, int64_t rows, const float* lse,
-                            const float* dloss, float* lse_eff, float* gscale, hipStream_t s);
-// P[t][index - v0] = exp(zk - lse) - p for the entries inside [v0, v0 + width)
+// the gradient's terms at the named entries (see head.hip)
+hipError_t launch_head_entries(const HeadTargets& tg, int64_t m, int64_t rows, const float* zk,
+                               const float* lse, const float* dloss, float* lse_eff,
+                               float* gscale, _Float16* dz16, float* rest, hipStream_t s);
+// P[t][index - v0] = dz16 for the entries inside [v0, v0 + width)
 hipError_t launch_head_scatter(const HeadTargets& tg, int64_t m, int64_t rows, int64_t v0,
-                               int64_t width, const float* zk, const float* lse, _Float16* P,
-                               int64_t ldp, hipStream_t s);
+                               int64_t width, const _Float16* dz16, _Float16* P, int64_t ldp,
+                               hipStream_t s);
+// sums[t] = sum_k rest[t][k] W_hat[index[t][k]]
+hipError_t launch_head_rest(int bits, const HeadTargets& tg, int64_t m, const uint32_t* packed,
+                            int64_t cols, const float* scales, const float* zeros, int groupsize,
+                            const float* rest, float* sums, hipStream_t s);
 constexpr int kSweepRows = 16;  // rows per sweep workgroup
 constexpr int kBlock = 128;     // columns per block
 constexpr int kSuperBlock = 512;  // columns per superblock of the two-level lazy update

@@ -290,7 +290,6 @@ struct GemmOut {
   int64_t ldc;
   float* c32;          // m x n
   const float* scale;  // m
-  bool first;          // c32 holds nothing yet
   float* sums;         // splits x m x n
 };
 
@@ -391,7 +390,7 @@ __global__ __launch_bounds__(512, 1) void gemm_nt_kernel(const _Float16* __restr
 #pragma unroll
           for (int b = 0; b < BT; ++b) {
             const int64_t c = nw + 16 * b + li;
-            if (!o.first && c < n) acc[a][b][i] += o.c32[t * n + c];
+            if (c < n) acc[a][b][i] += o.c32[t * n + c];
             acc[a][b][i] *= o.scale[t];
           }
         }
@@ -410,12 +409,11 @@ __global__ __launch_bounds__(512, 1) void gemm_nt_kernel(const _Float16* __restr
       for (int b = 0; b < BT; ++b) {
         const int64_t c = nw + 16 * b + li;
         if (c >= n) continue;
-        float v = acc[a][b][i];
+        const float v = acc[a][b][i];
         if constexpr (MODE == kSplit) {
           o.sums[((int64_t)blockIdx.y * m + t) * n + c] = v;
         } else {
-          if (!o.first) v += o.c32[t * n + c];
-          o.c32[t * n + c] = v;
+          o.c32[t * n + c] += v;
         }
       }
     }
@@ -432,7 +430,7 @@ __global__ __launch_bounds__(256) void gemm_reduce_kernel(int splits, int64_t m,
   for (int k = 0; k < splits; ++k) v += o.sums[(k * m + t) * n + c];
   if constexpr (MODE == kStoreAdapters) v += low_rank(o.ad, t, c, vec_up(o.ad));
   if constexpr (MODE == kAccumulate || MODE == kFinish)
-    if (!o.first) v += o.c32[t * n + c];
+    v += o.c32[t * n + c];
   if constexpr (MODE == kAccumulate) o.c32[t * n + c] = v;
   else o.c16[t * o.ldc + c] = (_Float16)(MODE == kFinish ? o.scale[t] * v : v);
 }
@@ -555,7 +553,7 @@ hipError_t launch_gemm_nt_f16(const _Float16* A, int64_t lda, int64_t m, const _
 }
 
 hipError_t launch_gemm_nt_acc(const _Float16* A, int64_t lda, int64_t m, const _Float16* B,
-                              int64_t ldb, int64_t n, int64_t K, bool first, float* C32,
+                              int64_t ldb, int64_t n, int64_t K, float* C32,
                               const float* scale, float* sums, _Float16* C16, int64_t ldc,
                               hipStream_t s) {
   GemmOut o{};
@@ -564,7 +562,6 @@ hipError_t launch_gemm_nt_acc(const _Float16* A, int64_t lda, int64_t m, const _
   o.ldc = ldc;
   o.c32 = C32;
   o.scale = scale;
-  o.first = first;
   if (C16 == nullptr) return launch_gemm<kAccumulate>(A, lda, m, B, ldb, n, K, o, s);
   return launch_gemm<kFinish>(A, lda, m, B, ldb, n, K, o, s);
 }

@@ -95,44 +95,130 @@ __global__ __launch_bounds__(256) void head_finish_kernel(int64_t m, int64_t row
   }
 }
 
-__global__ __launch_bounds__(256) void head_rows_kernel(HeadTargets tg, int64_t m, int64_t rows,
-                                                        const float* __restrict__ lse,
-                                                        const float* __restrict__ dloss,
-                                                        float* __restrict__ lse_eff,
-                                                        float* __restrict__ gscale) {
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (t >= m) return;
-  bool any = false;
-  for (int k = 0; k < tg.top && !any; ++k) any = takes_part(tg, t, k, rows);
-  lse_eff[t] = any ? lse[t] : INFINITY;
-  gscale[t] = any ? dloss[t] * tg.inv_t : 0.f;
-}
-
-// An index named by several entries gets their sum from each of them (the
-// same value, written more than once).
-__global__ __launch_bounds__(64) void head_scatter_kernel(HeadTargets tg, int64_t rows, int64_t v0,
-                                                          int64_t width,
-                                                          const float* __restrict__ zk,
-                                                          const float* __restrict__ lse,
-                                                          _Float16* __restrict__ P, int64_t ldp) {
-  __shared__ int idx[kMaxTop];
-  __shared__ float prob[kMaxTop];
-  const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x;
+// The gradient at the named entries, dz_k = exp(z_k - lse) - sum of their
+// probabilities (an index named by several entries gets the sum from each of
+// them), in fp32; one token per wave.  dz16 is what the product takes, rest =
+// dz - dz16 what its rounding leaves (0 for a repeated index but the first,
+// and for entries under 1/32 of the token's largest, whose roundings are as
+// much smaller).  Also lse_eff = lse or +inf and gscale = dloss inv_t or 0, for
+// tokens with and without entries.
+__global__ __launch_bounds__(256) void head_entries_kernel(
+    HeadTargets tg, int64_t m, int64_t rows, const float* __restrict__ zk,
+    const float* __restrict__ lse, const float* __restrict__ dloss, float* __restrict__ lse_eff,
+    float* __restrict__ gscale, _Float16* __restrict__ dz16, float* __restrict__ rest) {
+  __shared__ int idx[4][kMaxTop];
+  __shared__ float prob[4][kMaxTop];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t t = min((int64_t)blockIdx.x * 4 + wave, m - 1);  // (the last ones again)
   bool any;
   const float tlse = teacher_lse(tg, t, rows, &any);
   for (int k = lane; k < tg.top; k += 64) {
     const bool in = takes_part(tg, t, k, rows);
-    idx[k] = in ? tg.index[t * tg.top + k] : -1;
-    prob[k] = in ? __expf(log_p(tg, t, k, tlse)) : 0.f;
+    idx[wave][k] = in ? tg.index[t * tg.top + k] : -1;
+    prob[wave][k] = in ? __expf(log_p(tg, t, k, tlse)) : 0.f;
   }
   __syncthreads();
-  for (int k = lane; k < tg.top; k += 64) {
-    const int v = idx[k];
-    if (v < v0 || v >= v0 + width) continue;  // v0 >= 0: not an entry that is out
+  const float l = lse[t];
+  float dz[kMaxTop / 64], top = 0.f;
+  bool mine[kMaxTop / 64];
+#pragma unroll
+  for (int u = 0; u < kMaxTop / 64; ++u) {
+    const int k = lane + 64 * u;
+    dz[u] = 0.f;
+    mine[u] = false;
+    if (k >= tg.top || idx[wave][k] < 0) continue;
+    const int v = idx[wave][k];
     float p = 0.f;
-    for (int o = 0; o < tg.top; ++o) p += idx[o] == v ? prob[o] : 0.f;
-    P[t * ldp + v - v0] = (_Float16)(__expf(zk[t * tg.top + k] - lse[t]) - p);
+    bool first = true;
+    for (int o = 0; o < tg.top; ++o)
+      if (idx[wave][o] == v) {
+        p += prob[wave][o];
+        first = first && o >= k;
+      }
+    dz[u] = __expf(zk[t * tg.top + k] - l) - p;
+    mine[u] = first;
+    top = fmaxf(top, __builtin_fabsf(dz[u]));
+  }
+  top = wave_max(top);
+#pragma unroll
+  for (int u = 0; u < kMaxTop / 64; ++u) {
+    const int k = lane + 64 * u;
+    if (k >= tg.top) continue;
+    const _Float16 h = (_Float16)dz[u];
+    dz16[t * tg.top + k] = h;
+    rest[t * tg.top + k] =
+        mine[u] && __builtin_fabsf(dz[u]) * 32.f >= top ? dz[u] - (float)h : 0.f;
+  }
+  if (lane == 0) {
+    lse_eff[t] = any ? l : INFINITY;
+    gscale[t] = any ? dloss[t] * tg.inv_t : 0.f;
+  }
+}
+
+// The named entries' dz16 into one piece of the probabilities.
+__global__ __launch_bounds__(256) void head_scatter_kernel(HeadTargets tg, int64_t m, int64_t rows,
+                                                           int64_t v0, int64_t width,
+                                                           const _Float16* __restrict__ dz16,
+                                                           _Float16* __restrict__ P, int64_t ldp) {
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= m * tg.top) return;
+  const int64_t t = e / tg.top;
+  const int64_t v = tg.index[e];
+  if (v >= v0 && v < v0 + width && takes_part(tg, t, (int)(e % tg.top), rows))
+    P[t * ldp + v - v0] = dz16[e];
+}
+
+// sums[t] = sum_k rest[t][k] W_hat[index[t][k]] in fp32, what the entries'
+// rounding leaves out of the product (their dz are the gradient's largest
+// terms, and W_hat and dh are rounded already: without this dh is 1.65 times a
+// single rounding off).  One token per workgroup, a word (4 bits) or two (8)
+// of the rows per thread and turn; bound by the rows' reads from the caches.
+template <int BITS>
+__global__ __launch_bounds__(256) void head_rest_kernel(
+    HeadTargets tg, const uint32_t* __restrict__ packed, int64_t nw, int64_t cols,
+    const float* __restrict__ scales, const float* __restrict__ zeros, int64_t ngroups,
+    int groupsize, const float* __restrict__ rest, float* __restrict__ sums) {
+  constexpr int W = BITS / 4;  // words of 8 codes
+  constexpr uint32_t MASK = (1u << BITS) - 1u;
+  __shared__ int64_t row[kMaxTop];
+  __shared__ float weight[kMaxTop];
+  __shared__ int count;
+  const int64_t t = blockIdx.x;
+  if (threadIdx.x < 64) {  // the entries that have something, in order
+    int n = 0;
+    for (int k0 = 0; k0 < tg.top; k0 += 64) {
+      const int k = k0 + threadIdx.x;
+      const float r = k < tg.top ? rest[t * tg.top + k] : 0.f;
+      const unsigned long long b = __ballot(r != 0.f);  // (true for NaN)
+      if (r != 0.f) {
+        const int at = n + __popcll(b & ((1ull << threadIdx.x) - 1));
+        row[at] = tg.index[t * tg.top + k];
+        weight[at] = r;
+      }
+      n += __popcll(b);
+    }
+    if (threadIdx.x == 0) count = n;
+  }
+  __syncthreads();
+  const int n = count;
+  for (int64_t c = (int64_t)threadIdx.x * 8; c < cols; c += 256 * 8) {
+    const int64_t g = c / groupsize;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const int64_t r = row[i];
+      uint32_t q[W];
+#pragma unroll
+      for (int w = 0; w < W; ++w) q[w] = packed[r * nw + c * BITS / 32 + w];
+      const float s = scales[r * ngroups + g] * weight[i], z = zeros[r * ngroups + g];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        acc[j] = __builtin_fmaf(
+            s, (float)((q[j * BITS / 32] >> (j * BITS % 32)) & MASK) - z, acc[j]);
+    }
+    float4* out = reinterpret_cast<float4*>(sums + t * cols + c);
+    out[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    out[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
   }
 }
 
@@ -145,18 +231,32 @@ hipError_t launch_head_finish(int64_t m, int64_t rows, const HeadTargets& tg, co
   return hipGetLastError();
 }
 
-hipError_t launch_head_rows(const HeadTargets& tg, int64_t m, int64_t rows, const float* lse,
-                            const float* dloss, float* lse_eff, float* gscale, hipStream_t s) {
-  hipLaunchKernelGGL(head_rows_kernel, dim3((unsigned)ceil_div(m, 256)), dim3(256), 0, s, tg, m,
-                     rows, lse, dloss, lse_eff, gscale);
+hipError_t launch_head_entries(const HeadTargets& tg, int64_t m, int64_t rows, const float* zk,
+                               const float* lse, const float* dloss, float* lse_eff,
+                               float* gscale, _Float16* dz16, float* rest, hipStream_t s) {
+  hipLaunchKernelGGL(head_entries_kernel, dim3((unsigned)ceil_div(m, 4)), dim3(256), 0, s, tg, m,
+                     rows, zk, lse, dloss, lse_eff, gscale, dz16, rest);
   return hipGetLastError();
 }
 
 hipError_t launch_head_scatter(const HeadTargets& tg, int64_t m, int64_t rows, int64_t v0,
-                               int64_t width, const float* zk, const float* lse, _Float16* P,
-                               int64_t ldp, hipStream_t s) {
-  hipLaunchKernelGGL(head_scatter_kernel, dim3((unsigned)m), dim3(64), 0, s, tg, rows, v0, width,
-                     zk, lse, P, ldp);
+                               int64_t width, const _Float16* dz16, _Float16* P, int64_t ldp,
+                               hipStream_t s) {
+  hipLaunchKernelGGL(head_scatter_kernel, dim3((unsigned)ceil_div(m * tg.top, 256)), dim3(256), 0, s,
+                     tg, m, rows, v0, width, dz16, P, ldp);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_rest(int bits, const HeadTargets& tg, int64_t m, const uint32_t* packed,
+                            int64_t cols, const float* scales, const float* zeros, int groupsize,
+                            const float* rest, float* sums, hipStream_t s) {
+  const int64_t nw = packed_words(cols, bits), ng = ceil_div(cols, groupsize);
+  if (bits == 4)
+    hipLaunchKernelGGL(head_rest_kernel<4>, dim3((unsigned)m), dim3(256), 0, s, tg, packed, nw, cols,
+                       scales, zeros, ng, groupsize, rest, sums);
+  else
+    hipLaunchKernelGGL(head_rest_kernel<8>, dim3((unsigned)m), dim3(256), 0, s, tg, packed, nw, cols,
+                       scales, zeros, ng, groupsize, rest, sums);
   return hipGetLastError();
 }
 

@@ -82,26 +82,28 @@ BackwardLayout backward_layout(int64_t m, int64_t rows, int64_t cols, int64_t co
 }
 
 struct HeadLayout {
-  int64_t tokens, width, pieces;  // tokens and vocabulary entries per pass, passes over the latter
-  size_t lse, scale, probs, wt, acc, sums, scales, total;
+  int64_t tokens, width;  // tokens and vocabulary entries per pass
+  size_t lse, scale, dz, rest, probs, wt, acc, sums, scales, total;
 };
 
 // A pass keeps at most 2^25 probabilities (64 MB, which the 256 MB Infinity
-// Cache holds until the product reads them) of at most 8192 entries.
-HeadLayout head_layout(int64_t m, int64_t rows, int64_t cols) {
+// Cache holds until the product reads them) and 2^26 transposed weights.
+HeadLayout head_layout(int64_t m, int64_t rows, int64_t cols, int top) {
   HeadLayout L{};
   Carve c;
   L.tokens = m < kHeadTokens ? m : kHeadTokens;
   int64_t w = ((int64_t)1 << 25) / L.tokens / 256 * 256;
-  if (w > 8192) w = 8192;
+  const int64_t by_weights = most(((int64_t)1 << 26) / cols / 256 * 256, 256);
+  if (w > by_weights) w = by_weights;
   if (w > round_up(rows, 256)) w = round_up(rows, 256);
   L.width = w;
-  L.pieces = ceil_div(rows, w);
   L.lse = c.take(m, 4);
   L.scale = c.take(m, 4);
   L.probs = c.take(L.tokens * gemm_pitch(w), 2);
   L.wt = c.take(cols * gemm_pitch(w), 2);
-  L.acc = c.take(L.pieces > 1 ? L.tokens * cols : 0, 4);
+  L.acc = c.take(L.tokens * cols, 4);
+  L.dz = c.take(m * top, 2);
+  L.rest = c.take(m * top, 4);
   // the last pass over the tokens may split more than the others
   const int64_t rest = m % L.tokens;
   L.sums = c.take(most(split_sums(L.tokens, cols, w), rest > 0 ? split_sums(rest, cols, w) : 0), 4);
@@ -377,12 +379,12 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
   return GPTQ_OK;
 }
 
-size_t gptq_head_workspace_bytes(int op, int64_t m, int64_t rows, int64_t cols) {
-  if (m < 1 || m > kMaxTokens || rows < 1 || cols < 1 || rows > kMaxDim || cols > kMaxDim) return 0;
+size_t gptq_head_workspace_bytes(int op, int64_t m, int64_t rows, int64_t cols, int top) {
+  if (m < 1 || top < 1 || top > kMaxTop || m > kMaxTokens || rows < 1 || cols < 1 || rows > kMaxDim || cols > kMaxDim) return 0;
   switch (op) {
     case GPTQ_OP_HEAD_LOSS:
       return partials_bytes(m, rows) + align_up((size_t)scales_copy(m, rows, cols) * sizeof(float));
-    case GPTQ_OP_HEAD_BACKWARD: return head_layout(m, rows, cols).total;
+    case GPTQ_OP_HEAD_BACKWARD: return head_layout(m, rows, cols, top).total;
     default: return 0;
   }
 }
@@ -424,7 +426,8 @@ gptq_status head_forward(const void* h, int64_t m, int64_t cols, int64_t ldh,
     return GPTQ_ERR_UNSUPPORTED;
   if (m == 0) return GPTQ_OK;
   const gptq_status ok = workspace_ok(workspace, workspace_bytes,
-                                      gptq_head_workspace_bytes(GPTQ_OP_HEAD_LOSS, m, rows, cols));
+                                      gptq_head_workspace_bytes(GPTQ_OP_HEAD_LOSS, m, rows, cols,
+                                                                top));
   if (ok != GPTQ_OK) return ok;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const _Float16* x = reinterpret_cast<const _Float16*>(h);
@@ -456,7 +459,7 @@ gptq_status head_backward(const void* h, int64_t m, int64_t cols, int64_t ldh,
       !linear_forward_supported(bits, m, rows, cols, groupsize, h, m > 0 ? ldh : 8, packed))
     return GPTQ_ERR_UNSUPPORTED;
   if (m == 0) return GPTQ_OK;
-  const HeadLayout L = head_layout(m, rows, cols);
+  const HeadLayout L = head_layout(m, rows, cols, top);
   const gptq_status ok = workspace_ok(workspace, workspace_bytes, L.total);
   if (ok != GPTQ_OK) return ok;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -467,7 +470,9 @@ gptq_status head_backward(const void* h, int64_t m, int64_t cols, int64_t ldh,
   _Float16* wt = reinterpret_cast<_Float16*>(ws + L.wt);
   float* acc = reinterpret_cast<float*>(ws + L.acc);
   const int64_t nw = packed_words(cols, bits), ng = ceil_div(cols, groupsize);
-  GPTQ_TRY(launch_head_rows(tg, m, rows, lse, dloss, lse_eff, gscale, s));
+  _Float16* dz = reinterpret_cast<_Float16*>(ws + L.dz);
+  float* rest = reinterpret_cast<float*>(ws + L.rest);
+  GPTQ_TRY(launch_head_entries(tg, m, rows, zk, lse, dloss, lse_eff, gscale, dz, rest, s));
   for (int64_t t0 = 0; t0 < m; t0 += L.tokens) {
     const int64_t mt = m - t0 < L.tokens ? m - t0 : L.tokens;
     const _Float16* x = reinterpret_cast<const _Float16*>(h) + t0 * ldh;
@@ -475,6 +480,8 @@ gptq_status head_backward(const void* h, int64_t m, int64_t cols, int64_t ldh,
     HeadTargets tt = tg;
     tt.index += t0 * top;
     if (tt.logits != nullptr) tt.logits += t0 * top;
+    GPTQ_TRY(launch_head_rest(bits, tt, mt, packed, cols, scales, zeros, groupsize, rest + t0 * top,
+                              acc, s));
     for (int64_t v0 = 0; v0 < rows; v0 += L.width) {
       const int64_t w = rows - v0 < L.width ? rows - v0 : L.width;
       const int64_t wp = round_up(w, kKPad), ld = gemm_pitch(wp);
@@ -482,10 +489,10 @@ gptq_status head_backward(const void* h, int64_t m, int64_t cols, int64_t ldh,
       GPTQ_TRY(launch_head_probs(bits, x, ldh, mt, packed + v0 * nw, w, cols, scales + v0 * ng,
                                  zeros + v0 * ng, groupsize, tg.inv_t, lse_eff + t0,
                                  reinterpret_cast<float*>(ws + L.scales), P, ld, s));
-      GPTQ_TRY(launch_head_scatter(tt, mt, rows, v0, w, zk + t0 * top, lse + t0, P, ld, s));
+      GPTQ_TRY(launch_head_scatter(tt, mt, rows, v0, w, dz + t0 * top, P, ld, s));
       GPTQ_TRY(launch_prepare(packed + v0 * nw, bits, w, cols, scales + v0 * ng, zeros + v0 * ng,
                               groupsize, nullptr, wp, ld, wt, nullptr, s));
-      GPTQ_TRY(launch_gemm_nt_acc(P, ld, mt, wt, ld, cols, wp, v0 == 0, acc, gscale + t0,
+      GPTQ_TRY(launch_gemm_nt_acc(P, ld, mt, wt, ld, cols, wp, acc, gscale + t0,
                                   reinterpret_cast<float*>(ws + L.sums), last ? out : nullptr, lddh,
                                   s));
     }

@@ -145,9 +145,11 @@ def test_distillation(env, m, rows, cols, bits, g, top, T):
 
 
 def test_several_pieces_of_the_vocabulary(env):
-    """20011 entries: three pieces, the last one ragged; then distillation."""
-    _case(env, 40, 20011, 256, 4, 128, 0, 1.0, seed=1)
-    _case(env, 40, 20011, 256, 4, 128, 16, 2.0, seed=2)
+    """2100 x 40011 probabilities: three pieces of the vocabulary, the last
+    one ragged; then 9001 x 8192 weights: two pieces. The largest tiles too,
+    in the products and the gradient."""
+    _case(env, 2100, 40011, 128, 4, 128, 0, 1.0, seed=1)
+    _case(env, 3, 9001, 8192, 4, 128, 16, 2.0, seed=2)
 
 
 def test_more_tokens_than_one_pass(env):
@@ -241,7 +243,8 @@ def test_any_stream_any_workspace_again_and_strided(env):
     wide = torch.full((m, 264), 9.0, dtype=torch.float16, device="cuda")
     wide[:, :256] = _cuda(env, h)
     hd = _cuda(env, h)
-    need = max(gq.head_workspace_bytes(op, m, 700, 256) for op in (gq.OP_HEAD_LOSS, gq.OP_HEAD_BACKWARD))
+    need = max(gq.head_workspace_bytes(op, m, 700, 256, 8)
+               for op in (gq.OP_HEAD_LOSS, gq.OP_HEAD_BACKWARD))
 
     def all_of(h, fill, stream, out=None):
         ws = None if fill is None else torch.full((need,), fill, dtype=torch.uint8, device="cuda")

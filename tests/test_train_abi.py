@@ -117,7 +117,7 @@ def test_head_refusals(kind):
         assert call(**b) == UNSUP, b
     assert call(m=0, h=None, index=None, dh=None) == gq.GPTQ_OK
     op = gq.OP_HEAD_BACKWARD if backward else gq.OP_HEAD_LOSS
-    need = gq.head_workspace_bytes(op, 4, 500, 256)
+    need = gq.head_workspace_bytes(op, 4, 500, 256, 8 if distill else 1)
     assert need > 0 and call() == WS and call(ws=FAKE, wsb=need - 1) == WS
     assert call(ws=FAKE + 64, wsb=need) == BAD
 
@@ -132,11 +132,12 @@ def test_workspace_sizes():
               (gq.OP_BACKWARD, 4, 64, 64, 1, 0), (99, 4, 64, 64, 1, 8)):
         assert wb(*a) == 0, a
     assert hb(gq.OP_HEAD_LOSS, 0, 500, 256) == 0 and hb(99, 4, 500, 256) == 0
-    # a gradient's workspace stops growing with the tokens' probabilities (8192
-    # tokens a pass) and with the vocabulary (8192 entries a pass)
+    assert hb(gq.OP_HEAD_LOSS, 4, 500, 256, 0) == 0 and hb(gq.OP_HEAD_LOSS, 4, 500, 256, 257) == 0
+    # a gradient's workspace stops growing with the tokens (8192 a pass; a few
+    # values per token and entry remain) and with the vocabulary (2^26 weights)
     big = hb(gq.OP_HEAD_BACKWARD, 1 << 20, 32000, 4096)
-    assert big < hb(gq.OP_HEAD_BACKWARD, 8192, 32000, 4096) + (1 << 20) * 8 + 4096
-    assert hb(gq.OP_HEAD_BACKWARD, 64, 1 << 20, 256) <= hb(gq.OP_HEAD_BACKWARD, 64, 1 << 17, 256)
+    assert big < hb(gq.OP_HEAD_BACKWARD, 8192, 32000, 4096) + (1 << 20) * 14 + 4096
+    assert hb(gq.OP_HEAD_BACKWARD, 64, 1 << 20, 256) <= hb(gq.OP_HEAD_BACKWARD, 64, 1 << 19, 256)
 
 
 def test_python_checks_come_before_the_library():
