@@ -40,7 +40,21 @@ struct Wide {
   static constexpr int STAGE = X_BYTES + W_BYTES + 2 * TN * 4;
   static constexpr int LPS = 4 + WU + 1;         // direct loads per wave and stage
   static constexpr int NW = BITS / 2;            // words per lane, output and stage
+  // The 16-byte pieces of a packed row change places with the row, so that a
+  // fragment read meets every bank once: 8 bytes of 32 lanes (rows of 32
+  // bytes, 4 bits), 16 bytes of 16 lanes (rows of 64 bytes, 8 bits).
+  __device__ static int piece(int row, int p) {
+    return BITS == 4 ? p ^ ((row >> 3) & 1) : p ^ ((row >> 2) & 3);
+  }
 };
+
+// The 16-byte pieces of a row of x (128 bytes) are permuted by the row: the
+// fp16 product's (row >> 1) & 7 with its bits turned, since here lane group kg
+// reads piece 2 kg + s and not 4 s + kg.
+__device__ inline int x_swizzle(int row) {
+  const int r = (row >> 1) & 7;
+  return ((r << 1) | (r >> 2)) & 7;
+}
 
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void lds_void;
@@ -220,12 +234,13 @@ __global__ __launch_bounds__(64 * NWAVE, 1) void linear_wide_kernel(LinearCall c
   for (int u = 0; u < 4; ++u) {
     const int row = 8 * (wave + NWAVE * u) + (lane >> 3);
     l.x[u] = (uint32_t)((min(t0 + row, m - 1) - t0) * c.ldx * 2 +
-                        16 * ((lane & 7) ^ ((row >> 1) & 7)));
+                        16 * ((lane & 7) ^ x_swizzle(row)));
   }
 #pragma unroll
   for (int u = 0; u < L::WU; ++u) {
     const int row = (64 / L::PPR) * (wave + NWAVE * u) + lane / L::PPR;
-    l.w[u] = (uint32_t)((min(n0 + row, rows - 1) - n0) * nw * 4 + 16 * (lane % L::PPR));
+    l.w[u] = (uint32_t)((min(n0 + row, rows - 1) - n0) * nw * 4 +
+                        16 * L::piece(row, lane % L::PPR));
   }
   l.sz = (uint32_t)((min(n0 + 64 * (wave & 3) + lane, rows - 1) - n0) * 4);
   const char* xb = reinterpret_cast<const char*>(c.x + t0 * c.ldx);
@@ -234,8 +249,9 @@ __global__ __launch_bounds__(64 * NWAVE, 1) void linear_wide_kernel(LinearCall c
   const int64_t szp = c.pitch_t * 4;
 
   // LDS offsets of this lane's fragments (a-tile a: + 2048 a, step s: ^ 16 s)
-  const int xo = (128 * wm + li) * 128 + 16 * ((2 * kg) ^ ((li >> 1) & 7));
-  const int wo = (64 * wn + li) * L::RB + L::NW * 4 * kg;
+  const int xo = (128 * wm + li) * 128 + 16 * ((2 * kg) ^ x_swizzle(li));
+  const int wo = (64 * wn + li) * L::RB +
+                 (BITS == 4 ? 16 * L::piece(li, kg >> 1) + 8 * (kg & 1) : 16 * L::piece(li, kg));
   const int so = 4 * (64 * wn + li);
 
   f32x4 acc[AT][BT];
