@@ -62,9 +62,18 @@ inline TileGrid linear_grid(int64_t ntm, int64_t ntn) {
 // Below, a workgroup of WM x WN waves holds 16 AT WM tokens x 16 BT WN outputs
 // from (t0, n0) on; this wave is (wm, wn).
 
-// (max, sum exp(z - max)) of the tile's outputs for each of its tokens: over
-// the wave's outputs in registers and 16-lane shuffles, over the waves through
-// LDS.  Outputs past the matrix count as -inf.
+// (max, sum exp(z - max)) of two sets of values as one's.
+__device__ inline void join(float& top, float& sum, float top2, float sum2) {
+  const float t = fmaxf(top, top2), base = t == -INFINITY ? 0.f : t;
+  sum = sum * __expf(top - base) + sum2 * __expf(top2 - base);
+  top = t;
+}
+
+// (max, sum exp(z - max)) of the tile's outputs for each of its tokens.  Every
+// lane takes its own BT outputs of 16 rows; four exchanges over its 16 lanes,
+// each halving the rows a lane keeps (8 + 4 + 2 + 1 pairs, where a butterfly
+// for every row takes 64), leave one row to a lane; the waves' are joined
+// through LDS.  Outputs past the matrix count as -inf.
 template <int AT, int BT, int WM, int WN>
 __device__ inline void tile_partials(const f32x4 (&acc)[AT][BT], const Tail& tail, float2* red,
                                      int64_t t0, int64_t m, int64_t tn, int64_t n0, int64_t rows,
@@ -73,54 +82,87 @@ __device__ inline void tile_partials(const f32x4 (&acc)[AT][BT], const Tail& tai
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, kg = lane >> 4;
   const int64_t nw = n0 + 16 * BT * wn;
 #pragma unroll
-  for (int a = 0; a < AT; ++a)
+  for (int c = 0; c < AT / 4; ++c) {
+    float top[16], sum[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float z[BT], top = -INFINITY;
+    for (int r = 0; r < 16; ++r) {
+      float z[BT];
+      top[r] = -INFINITY;
 #pragma unroll
       for (int b = 0; b < BT; ++b) {
-        z[b] = nw + 16 * b + li < rows ? acc[a][b][i] * tail.inv_t : -INFINITY;
-        top = fmaxf(top, z[b]);
+        z[b] = nw + 16 * b + li < rows ? acc[4 * c + r / 4][b][r % 4] * tail.inv_t : -INFINITY;
+        top[r] = fmaxf(top[r], z[b]);
       }
+      const float base = top[r] == -INFINITY ? 0.f : top[r];
+      sum[r] = 0.f;
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-      const float base = top == -INFINITY ? 0.f : top;
-      float sum = 0.f;
-#pragma unroll
-      for (int b = 0; b < BT; ++b) sum += __expf(z[b] - base);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-      if (li == 0) red[wn * TM + 16 * (AT * wm + a) + 4 * kg + i] = make_float2(top, sum);
+      for (int b = 0; b < BT; ++b) sum[r] += __expf(z[b] - base);
     }
+#pragma unroll
+    for (int half = 8; half > 0; half >>= 1) {  // also the lanes' distance
+      const bool up = (li & half) != 0;
+#pragma unroll
+      for (int r = 0; r < half; ++r) {
+        const float t = __shfl_xor(up ? top[r] : top[r + half], half, 64);
+        const float s = __shfl_xor(up ? sum[r] : sum[r + half], half, 64);
+        if (up) {
+          top[r] = top[r + half];
+          sum[r] = sum[r + half];
+        }
+        join(top[r], sum[r], t, s);
+      }
+    }
+    // row li of the 16: tile 4 c + li / 4, row 4 kg + li % 4 of it
+    red[wn * TM + 16 * (AT * wm + 4 * c + li / 4) + 4 * kg + li % 4] = make_float2(top[0], sum[0]);
+  }
   __syncthreads();
   if (tid < TM && t0 + tid < m) {
-    float top = -INFINITY;
+    float2 p = red[tid];
 #pragma unroll
-    for (int w = 0; w < WN; ++w) top = fmaxf(top, red[w * TM + tid].x);
-    const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < WN; ++w) {
-      const float2 p = red[w * TM + tid];
-      sum += p.y * (p.x == -INFINITY ? 0.f : __expf(p.x - base));
+    for (int w = 1; w < WN; ++w) {
+      const float2 q = red[w * TM + tid];
+      join(p.x, p.y, q.x, q.y);
     }
-    tail.part[tn * m + t0 + tid] = make_float2(top, sum);
+    tail.part[tn * m + t0 + tid] = p;
   }
 }
 
 // zk[t][k] = z[t][index[t][k]] for the named outputs inside the tile: 16
 // tokens' sums of every wave row at a time go through LDS, and every thread
-// looks its share of their entries up.
+// looks its share of their entries up, the entries of the next 16 tokens being
+// loaded meanwhile.
 template <int AT, int BT, int WM, int WN>
 __device__ inline void tile_targets(const f32x4 (&acc)[AT][BT], const Tail& tail, float* zs,
                                     int64_t t0, int64_t m, int64_t n0, int64_t rows, int wm,
                                     int wn) {
   constexpr int TN = 16 * BT * WN, PITCH = TN + 4;  // rows 4 banks apart
+  constexpr int THREADS = 64 * WM * WN, U = 4;      // entries per thread that are loaded ahead
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, kg = lane >> 4;
   const int64_t end = min(n0 + TN, rows);
+  const int each = 16 * tail.top, n = WM * each;
+  // entry e of step a: wave row e / each, token (e % each) / top of its 16
+  auto place = [&](int a, int e, int& row) -> int64_t {
+    const int w = e / each, r = e % each;
+    row = 16 * w + r / tail.top;
+    const int64_t t = t0 + 16 * (AT * w + a) + r / tail.top;
+    return e < n && t < m ? t * tail.top + r % tail.top : -1;
+  };
+  int next[U];
+  auto load = [&](int a) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      int row;
+      const int64_t at = place(a, tid + THREADS * u, row);
+      next[u] = at >= 0 ? tail.index[at] : -1;
+    }
+  };
+  load(0);
 #pragma unroll
   for (int a = 0; a < AT; ++a) {
-    if (t0 + 16 * a >= m) break;
+    int now[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) now[u] = next[u];
+    if (a + 1 < AT) load(a + 1);
     __syncthreads();
 #pragma unroll
     for (int b = 0; b < BT; ++b)
@@ -129,16 +171,17 @@ __device__ inline void tile_targets(const f32x4 (&acc)[AT][BT], const Tail& tail
         zs[(16 * wm + 4 * kg + i) * PITCH + 16 * (BT * wn + b) + li] = acc[a][b][i];
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < WM; ++w) {
-      const int64_t t = t0 + 16 * (AT * w + a);
-      if (t >= m) break;
-      const int n = (int)min((int64_t)16, m - t) * tail.top;
-      const int64_t e0 = t * tail.top;
-      for (int e = tid; e < n; e += 64 * WM * WN) {
-        const int64_t v = tail.index[e0 + e];
-        if (v >= n0 && v < end)
-          tail.zk[e0 + e] = zs[(16 * w + e / tail.top) * PITCH + (v - n0)] * tail.inv_t;
+    for (int u = 0; u < U; ++u)
+      if (now[u] >= n0 && now[u] < end) {
+        int row;
+        const int64_t at = place(a, tid + THREADS * u, row);
+        tail.zk[at] = zs[row * PITCH + (now[u] - n0)] * tail.inv_t;
       }
+    for (int e = tid + THREADS * U; e < n; e += THREADS) {
+      int row;
+      const int64_t at = place(a, e, row);
+      const int v = at >= 0 ? tail.index[at] : -1;
+      if (v >= n0 && v < end) tail.zk[at] = zs[row * PITCH + (v - n0)] * tail.inv_t;
     }
   }
 }
