@@ -523,11 +523,12 @@ def head_workspace_bytes(op: int, m: int, rows: int, cols: int, top: int = 1) ->
 
 def _rows_of(t, m, n, dtype, dev, name):
     """An m x n matrix with unit column stride on GPU dev; returns its row stride."""
-    if t.dtype is not dtype or t.shape != (m, n) or t.get_device() != dev or \
-            (n > 1 and m > 0 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be an {m} x {n} {dtype} tensor with unit column stride "
-                         f"on cuda:{dev}")
-    return t.stride(0) if m > 1 else n
+    if t.dtype is dtype and t.shape == (m, n) and t.get_device() == dev:
+        ld, one = t.stride()
+        if one == 1 or n <= 1 or m == 0:
+            return ld if m > 1 else n
+    raise ValueError(f"{name} must be an {m} x {n} {dtype} tensor with unit column stride "
+                     f"on cuda:{dev}")
 
 
 def _exactly(t, shape, dtype, dev, name):
@@ -537,12 +538,12 @@ def _exactly(t, shape, dtype, dev, name):
 
 
 def _input(x, n, name):
-    """(tokens, row stride, GPU index) of an fp16 input with n columns."""
-    if x.dtype is not _f16 or x.dim() != 2 or not x.is_cuda or n is not None and x.shape[1] != n:
-        raise ValueError(f"{name} must be a 2-D fp16 CUDA tensor with unit column stride"
-                         + ("" if n is None else f" and {n} columns"))
-    dev, (m, n) = x.get_device(), x.shape
-    return m, _rows_of(x, m, n, _f16, dev, name), dev
+    """(tokens, row stride, GPU index) of an fp16 input with n columns (None: any)."""
+    shape, dev = x.shape, x.get_device()
+    if len(shape) == 2 and dev >= 0 and (n is None or shape[1] == n):
+        return shape[0], _rows_of(x, *shape, _f16, dev, name), dev
+    raise ValueError(f"{name} must be a 2-D fp16 CUDA tensor with unit column stride"
+                     + ("" if n is None else f" and {n} columns"))
 
 
 def _layer(packed, bits, cols, scales, zeros, groupsize, dev, g_idx=None):

@@ -43,9 +43,9 @@ namespace {
 constexpr int KG = 128;    // input columns per stage
 constexpr int NSTAGE = 3;
 
-// What depends on the code width: a wave's outputs (WTN), the packed bytes of
-// one output row per stage (RB), and the 16-byte pieces per lane per stage
-// (LP).  `piece` is the XOR swizzle of the 16-byte
+// What depends on the code width: a wave's outputs with many tokens (WTN), the
+// packed bytes of one output row per stage (RB), and the 16-byte pieces per
+// lane per stage (LP).  `piece` is the XOR swizzle of the 16-byte
 // pieces of a stage's packed row: the 16-byte reads of 16 consecutive rows at
 // one logical piece hit distinct bank groups, for 8- and for 16-lane LDS
 // service groups.
@@ -66,18 +66,19 @@ struct Geo<8> {
   __device__ static int piece(int row, int p) { return p ^ ((row ^ (row >> 3)) & 7); }
 };
 
-// A workgroup of W waves owns 16 A tokens x W * WTN outputs (every wave all of
-// the tokens).  <8, 8>, 128 tokens x 256 (4 bits) or 128 (8 bits) outputs, is
-// the shape for many tokens.
-template <int BITS_, int A, int W>
+// A workgroup of eight waves owns 16 A tokens x 8 N outputs, N of them a wave
+// (every wave all of the tokens).  A = 8 and the code width's N, 128 tokens x
+// 256 (4 bits) or 128 (8 bits) outputs, is the shape for many tokens; 64
+// tokens x 128 outputs the one for a few.
+template <int BITS_, int A, int N>
 struct Lay {
   static constexpr int BITS = BITS_;
-  static constexpr int AT = A, NWAVE = W, TM = 16 * A;
+  static constexpr int AT = A, NWAVE = 8, TM = 16 * A;
   static constexpr int RB = Geo<BITS>::RB, LP = Geo<BITS>::LP;
-  static constexpr int WTN = Geo<BITS>::WTN, TN = W * WTN;
+  static constexpr int WTN = N, TN = NWAVE * WTN;
   static constexpr int X_BYTES = TM * KG * 2;  // 32 KB at 128 tokens
   static constexpr int PPR = RB / 16;          // pieces per packed row
-  static constexpr int B_BYTES = TN * RB;      // 16 KB with eight waves
+  static constexpr int B_BYTES = TN * RB;      // 16 KB (few tokens: 8 KB at 4 bits)
   static constexpr int S_BYTES = TN * 4;       // scales (zeros follow)
   static constexpr int STAGE = X_BYTES + B_BYTES + 2 * S_BYTES;
   static constexpr int BT = WTN / 16;          // b-tiles per wave
@@ -86,7 +87,7 @@ struct Lay {
   static constexpr int WU = B_BYTES / 1024 / NWAVE;  // word loads per wave per stage
   static constexpr int SZL = 2 * S_BYTES / 256;      // 256-byte scale/zero loads per stage
   static constexpr int LOADS_PER_STAGE = XU + WU + 1;
-  static_assert(WU == 2 && XU >= 1 && XU * 1024 * NWAVE == X_BYTES && SZL >= 2 && SZL <= NWAVE,
+  static_assert(WU >= 1 && XU >= 1 && XU * 1024 * NWAVE == X_BYTES && SZL >= 2 && SZL <= NWAVE,
                 "stage layout");
 };
 
@@ -368,13 +369,13 @@ __device__ inline void stage_step(int k, int nk, const char* cur, char* nxt, con
 // start is the better one (4096 tokens: 307 against 315 us for 8192 outputs).
 // The layer's own product (kStore) always has xm = 8: its order of addition
 // does not depend on the tokens.
-template <int BITS, bool RELU, int TAIL, int A, int W>
-__global__ __launch_bounds__(64 * W, 1) void linear_kernel(
+template <int BITS, bool RELU, int TAIL, int A, int N>
+__global__ __launch_bounds__(512, 1) void linear_kernel(
     const _Float16* __restrict__ x, int64_t ldx, int64_t m, const uint32_t* __restrict__ packed,
     int64_t nw, int64_t rows, int64_t cols, const float* __restrict__ scales,
     const float* __restrict__ zeros, int64_t ngroups, int gk, TileGrid grid,
     _Float16* __restrict__ y, int64_t ldy, Tail tail) {
-  using L = Lay<BITS, A, W>;
+  using L = Lay<BITS, A, N>;
   constexpr int AT = L::AT, BT = L::BT;
   __shared__ __attribute__((aligned(1024))) char st0[L::STAGE];
   __shared__ __attribute__((aligned(1024))) char st1[L::STAGE];
@@ -418,24 +419,26 @@ __global__ __launch_bounds__(64 * W, 1) void linear_kernel(
       (sz_load<L>(wave) < L::SZL / 2 ? scales : zeros) + n0 * ngroups);
 
   GroupCursor use(start, gk), iss(start, gk);
-  issue_stage<L>(xb, wbase, szb, dm, iss.chunk, iss.grp, st0, wave);
-  iss.advance(gk, kb, ke, gb);
-  if (nk > 1) {
-    issue_stage<L>(xb, wbase, szb, dm, iss.chunk, iss.grp, st1, wave);
-    iss.advance(gk, kb, ke, gb);
-  }
   bool fold = false;
   float fsc[BT];
-  for (int k = 0; k < nk; k += NSTAGE) {
-    stage_step<L>(k, nk, st0, st2, xb, wbase, szb, dm, gk, kb, ke, gb, use, iss, wave, lo, acc,
-                  part, fold, fsc);
-    if (k + 1 < nk)
-      stage_step<L>(k + 1, nk, st1, st0, xb, wbase, szb, dm, gk, kb, ke, gb, use, iss, wave, lo,
-                    acc, part, fold, fsc);
-    if (k + 2 < nk)
-      stage_step<L>(k + 2, nk, st2, st1, xb, wbase, szb, dm, gk, kb, ke, gb, use, iss, wave, lo,
-                    acc, part, fold, fsc);
+#define GPTQ_ISSUE(N, ST)                                                \
+  if (N < nk) {                                                          \
+    issue_stage<L>(xb, wbase, szb, dm, iss.chunk, iss.grp, ST, wave);    \
+    iss.advance(gk, kb, ke, gb);                                         \
   }
+#define GPTQ_STAGE(N, CUR, NXT)                                                                   \
+  if (k + N < nk)                                                                                 \
+    stage_step<L>(k + N, nk, CUR, NXT, xb, wbase, szb, dm, gk, kb, ke, gb, use, iss, wave, lo, acc, \
+                  part, fold, fsc);
+  GPTQ_ISSUE(0, st0)
+  GPTQ_ISSUE(1, st1)
+  for (int k = 0; k < nk; k += NSTAGE) {
+    GPTQ_STAGE(0, st0, st2)
+    GPTQ_STAGE(1, st1, st0)
+    GPTQ_STAGE(2, st2, st1)
+  }
+#undef GPTQ_ISSUE
+#undef GPTQ_STAGE
   fold_group<AT, BT>(acc, part, fsc);  // the last stage always ends a group
 
   LinearCall c{};
@@ -443,7 +446,7 @@ __global__ __launch_bounds__(64 * W, 1) void linear_kernel(
   c.rows = rows;
   c.y = y;
   c.ldy = ldy;
-  tile_tail<RELU, TAIL, AT, BT, 1, W>(acc, tail, c, t0, n0, tn, 0, wave, st0, st1);
+  tile_tail<RELU, TAIL, AT, BT, 1, 8>(acc, tail, c, t0, n0, tn, 0, wave, st0, st1);
 }
 
 // The splits of a product added in order, the adapters' part, ReLU, fp16.
@@ -469,24 +472,25 @@ int64_t linear_blocks(int bits, int64_t m, int64_t rows) {
   return store_grid(ceil_div(m, 128), ceil_div(rows, 8 * (bits == 4 ? 32 : 16))).blocks();
 }
 
-template <int BITS, bool RELU, int TAIL, int A, int W>
+template <int BITS, bool RELU, int TAIL, int A, int N>
 hipError_t launch_tile(const LinearCall& c, const Tail& tail, int splits, hipStream_t s) {
   const int g = c.groupsize >= c.cols ? (int)c.cols : c.groupsize;
   const int64_t ngroups = ceil_div(c.cols, g);
   const int gk = (int)ceil_div(g, KG);  // chunks per group (a short last group ends at cols)
   const int64_t nw = c.cols * BITS / 32;
-  using L = Lay<BITS, A, W>;
+  using L = Lay<BITS, A, N>;
   const int64_t ntm = ceil_div(c.m, L::TM), ntn = ceil_div(c.rows, L::TN);
   const TileGrid grid = TAIL == kStore ? store_grid(ntm, ntn) : linear_grid(ntm, ntn);
-  hipLaunchKernelGGL((linear_kernel<BITS, RELU, TAIL, A, W>),
-                     dim3((unsigned)grid.blocks(), (unsigned)splits), dim3(64 * W), 0, s, c.x,
+  hipLaunchKernelGGL((linear_kernel<BITS, RELU, TAIL, A, N>),
+                     dim3((unsigned)grid.blocks(), (unsigned)splits), dim3(512), 0, s, c.x,
                      c.ldx, c.m, c.packed, nw, c.rows, c.cols, c.scales, c.zeros, ngroups, gk, grid,
                      c.y, c.ldy, tail);
   return hipGetLastError();
 }
 
-// The tile by the tokens and outputs: 64 tokens x 128 (64) outputs with four
-// waves up to 64 tokens; else 128 x 256 (128), or 256 x 256 where that takes
+// The tile by the tokens and outputs: 64 tokens x 128 outputs up to 64 tokens
+// (with four waves of 32 outputs, one per SIMD, building B and multiplying did
+// not overlap: 48 tokens x 32000 x 4096 took 42 us instead of XXX); else 128 x 256 (128), or 256 x 256 where that takes
 // less time.  A round of 256 workgroups of the latter takes 1.6 (8 bits: 2.2)
 // times one of the former.
 enum Shape { kFew, kMiddle, kWide };
@@ -503,17 +507,17 @@ hipError_t launch_tail(int bits, const LinearCall& c, const Tail& tail, int spli
                        hipStream_t s) {
   const Shape shape = shape_of(bits, c.m, c.rows);
   if (shape == kFew)
-    return bits == 4 ? launch_tile<4, RELU, TAIL, 4, 4>(c, tail, splits, s)
-                     : launch_tile<8, RELU, TAIL, 4, 4>(c, tail, splits, s);
+    return bits == 4 ? launch_tile<4, RELU, TAIL, 4, 16>(c, tail, splits, s)
+                     : launch_tile<8, RELU, TAIL, 4, 16>(c, tail, splits, s);
   if constexpr (TAIL != kSplit)
     if (shape == kWide) return launch_linear_wide<RELU, TAIL>(bits, c, tail, s);
-  return bits == 4 ? launch_tile<4, RELU, TAIL, 8, 8>(c, tail, splits, s)
-                   : launch_tile<8, RELU, TAIL, 8, 8>(c, tail, splits, s);
+  return bits == 4 ? launch_tile<4, RELU, TAIL, 8, 32>(c, tail, splits, s)
+                   : launch_tile<8, RELU, TAIL, 8, 16>(c, tail, splits, s);
 }
 
 int64_t tail_outputs(int bits, int64_t m, int64_t rows) {  // outputs per tile
   switch (shape_of(bits, m, rows)) {
-    case kFew: return 4 * (bits == 4 ? Geo<4>::WTN : Geo<8>::WTN);
+    case kFew: return 128;
     case kMiddle: return 8 * (bits == 4 ? Geo<4>::WTN : Geo<8>::WTN);
     default: return 256;
   }
@@ -555,10 +559,10 @@ hipError_t launch_linear_forward(int bits, const _Float16* x, int64_t ldx, int64
                      nullptr, nullptr, 0};
   const Tail t{};
   if (bits == 4)
-    return relu ? launch_tile<4, true, kStore, 8, 8>(c, t, 1, s)
-                : launch_tile<4, false, kStore, 8, 8>(c, t, 1, s);
-  return relu ? launch_tile<8, true, kStore, 8, 8>(c, t, 1, s)
-              : launch_tile<8, false, kStore, 8, 8>(c, t, 1, s);
+    return relu ? launch_tile<4, true, kStore, 8, 32>(c, t, 1, s)
+                : launch_tile<4, false, kStore, 8, 32>(c, t, 1, s);
+  return relu ? launch_tile<8, true, kStore, 8, 16>(c, t, 1, s)
+              : launch_tile<8, false, kStore, 8, 16>(c, t, 1, s);
 }
 
 int linear_splits(int bits, int64_t m, int64_t rows, int64_t cols, int groupsize) {
