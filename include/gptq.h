@@ -517,8 +517,8 @@ gptq_status gptq_linear_forward_adapters(const void* x, int64_t m, int64_t cols,
  *   2^-14; values beyond 65504 become infinite), products are exact in fp32
  *   and summed there, dv enters it held to 2^-23 of the largest of 16 of its
  *   values, and dx is rounded to fp16 once.  dA and dB are fp32 throughout;
- *   their sums run over an adapter's tokens in token order, 256 at a time, so
- *   results are bitwise reproducible.
+ *   their sums run over an adapter's tokens in token order, 256 (up to 1024
+ *   tokens: 64) at a time, so results are bitwise reproducible.
  *   Asynchronous.
  */
 gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_t lddy,

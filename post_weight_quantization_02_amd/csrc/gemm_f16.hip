@@ -38,7 +38,7 @@ struct Prepare {
   _Float16* at;
   const int* index;
   int64_t m;
-  int max_chunks;
+  int chunk, max_chunks;
   int* list;
   GradChunk* chunks;
   int2* ranges;
@@ -143,8 +143,8 @@ __device__ inline void transpose_down(const Prepare& p, int64_t bid) {
 }
 
 // Tokens grouped by adapter, in token order inside each (so the gradients'
-// sums have one order), and cut into chunks of at most kGradChunk tokens of
-// one adapter.  One workgroup per adapter: it counts every adapter's tokens
+// sums have one order), and cut into chunks of at most `chunk` tokens of one
+// adapter.  One workgroup per adapter: it counts every adapter's tokens
 // (integer LDS atomics), finds its own places and writes its own tokens, 16
 // adjacent ones a thread at a time.
 struct GroupShared {
@@ -166,7 +166,7 @@ __device__ inline void group_tokens(const Prepare& p, int a, GroupShared& sh) {
   if (wave == 0) {  // tokens and chunks of the adapters before this one
     int tokens = 0, before = 0, total = 0;
     for (int i = lane; i < count; i += 64) {
-      const int c = (sh.hist[i] + kGradChunk - 1) / kGradChunk;
+      const int c = (sh.hist[i] + p.chunk - 1) / p.chunk;
       total += c;
       if (i < a) {
         tokens += sh.hist[i];
@@ -178,14 +178,14 @@ __device__ inline void group_tokens(const Prepare& p, int a, GroupShared& sh) {
       before += __shfl_xor(before, o, 64);
       total += __shfl_xor(total, o, 64);
     }
-    const int mine = (sh.hist[a] + kGradChunk - 1) / kGradChunk;
+    const int mine = (sh.hist[a] + p.chunk - 1) / p.chunk;
     if (lane == 0) {
       sh.base = tokens;
       p.ranges[a] = make_int2(before, mine);
     }
     for (int c = lane; c < mine; c += 64)
-      p.chunks[before + c] = GradChunk{a, tokens + c * kGradChunk,
-                                       min(kGradChunk, sh.hist[a] - c * kGradChunk)};
+      p.chunks[before + c] =
+          GradChunk{a, tokens + c * p.chunk, min(p.chunk, sh.hist[a] - c * p.chunk)};
     if (a == 0)
       for (int c = total + lane; c < p.max_chunks; c += 64) p.chunks[c] = GradChunk{-1, 0, 0};
   }
@@ -516,6 +516,7 @@ hipError_t launch_prepare(const uint32_t* packed, int bits, int64_t rows, int64_
     p.at_blocks = ad->count * ceil_div(cols, 256);
     p.index = ad->index;
     p.m = ad->m;
+    p.chunk = grad_chunk(ad->m);
     p.max_chunks = (int)grad_chunks(ad->m, ad->count);
     p.list = ad->list;
     p.chunks = ad->chunks;

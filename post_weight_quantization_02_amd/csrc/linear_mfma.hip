@@ -490,7 +490,7 @@ hipError_t launch_tile(const LinearCall& c, const Tail& tail, int splits, hipStr
 
 // The tile by the tokens and outputs: 64 tokens x 128 outputs up to 64 tokens
 // (with four waves of 32 outputs, one per SIMD, building B and multiplying did
-// not overlap: 48 tokens x 32000 x 4096 took 42 us instead of XXX); else 128 x 256 (128), or 256 x 256 where that takes
+// not overlap: 48 tokens x 32000 x 4096 took 42 us instead of 38); else 128 x 256 (128), or 256 x 256 where that takes
 // less time.  A round of 256 workgroups of the latter takes 1.6 (8 bits: 2.2)
 // times one of the former.
 enum Shape { kFew, kMiddle, kWide };
