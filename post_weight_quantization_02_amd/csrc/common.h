@@ -203,6 +203,7 @@ struct PrepareAdapters {  // what the adapters' gradients need beside them
   GradChunk* chunks;
   int2* ranges;     // chunks of each adapter: first, number
 };
+// (wt NULL: without the weights)
 hipError_t launch_prepare(const uint32_t* packed, int bits, int64_t rows, int64_t cols,
                           const float* scales, const float* zeros, int groupsize, const int* g_idx,
                           int64_t kp, int64_t ldt, _Float16* wt, const PrepareAdapters* ad,
@@ -210,13 +211,27 @@ hipError_t launch_prepare(const uint32_t* packed, int bits, int64_t rows, int64_
 // dst[t][0 .. kp) = src[t][0 .. K) and zeros, row pitch ldd
 hipError_t launch_pad_rows(const _Float16* src, int64_t lds, int64_t m, int64_t K, int64_t kp,
                            int64_t ldd, _Float16* dst, hipStream_t s);
-// C = A B^T, A m x K, B n x K (K % kKPad == 0, 16-byte aligned rows)
+// The layer itself in B's place, where words_ok: few tokens do without a
+// transposed copy.  words_splits >= 1 splits of K, all through the workspace.
+struct StoredWeights {
+  const uint32_t* packed;
+  int bits;
+  int64_t rows, cols;
+  const float *scales, *zeros;
+  int groupsize;
+};
+bool words_ok(int64_t m, int bits, int64_t cols, int groupsize, const int* g_idx);
+int words_splits(int64_t m, int64_t n, int64_t K);
+// C = A B^T, A m x K, B n x K (K % kKPad == 0, 16-byte aligned rows; w: not
+// read)
 hipError_t launch_gemm_nt_f16(const _Float16* A, int64_t lda, int64_t m, const _Float16* B,
-                              int64_t ldb, int64_t n, int64_t K, const AdapterTile* ad,
+                              int64_t ldb, int64_t n, int64_t K, const StoredWeights* w,
+                              const AdapterTile* ad,
                               float* sums, _Float16* C, int64_t ldc, hipStream_t s);
 // C32 += A B^T, or with C16 the finished rows: C16 = fp16(scale[t] (C32 + A B^T))
 hipError_t launch_gemm_nt_acc(const _Float16* A, int64_t lda, int64_t m, const _Float16* B,
-                              int64_t ldb, int64_t n, int64_t K, float* C32,
+                              int64_t ldb, int64_t n, int64_t K, const StoredWeights* w,
+                              float* C32,
                               const float* scale, float* sums, _Float16* C16, int64_t ldc,
                               hipStream_t s);
 // splits of K when the tiles leave CUs idle (1: none); their fp32 sums,

@@ -435,6 +435,147 @@ __global__ __launch_bounds__(256) void gemm_reduce_kernel(int splits, int64_t m,
   else o.c16[t * o.ldc + c] = (_Float16)(MODE == kFinish ? o.scale[t] * v : v);
 }
 
+// ------------------------------------------------------- few tokens
+// The same product straight from the packed words, for the few tokens that
+// would not pay for a transposed copy of the weights: 64 WM tokens x 128
+// columns per workgroup and split of the rows (the product's K), 64 rows a
+// stage.  A thread takes the words of two adjacent rows, so that a code of
+// each makes the adjacent pair that a fragment wants: a byte of both words by
+// one v_perm_b32, 1024 + q by bit operations, q by one packed addition
+// (exact), and (q - z) * s in fp32, rounded to fp16 once: the transposed copy's
+// values, for any z.
+// Words, scales and A are loaded two stages ahead into registers, and a stage
+// is written to LDS while the one before is multiplied.
+//
+// 160 tokens x 4096 x 4096 at 8 bits: 24 us, where the transposition (19) and
+// the product from the copy (16) took 35; with the pieces in their own order
+// 34, with branches around the loads of the last stages 27.  Bound by latency: a split has 8
+// stages.
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+
+template <int BITS, int WM>
+__global__ __launch_bounds__(512, 2) void gemm_words_kernel(
+    const _Float16* __restrict__ A, int64_t lda, int64_t m, const uint32_t* __restrict__ packed,
+    int64_t nw, int64_t rows, int64_t n, int64_t K, const float* __restrict__ scales,
+    const float* __restrict__ zeros, int64_t ngroups, int groupsize, float* __restrict__ sums) {
+  constexpr int WN = 8 / WM, BT = 8 / WN, TM = 64 * WM, P = KC + 8;
+  constexpr int AU = TM / 64;          // 16-byte pieces of A per thread and stage
+  constexpr int W = BITS / 4;          // words per row and thread (8 columns)
+  __shared__ __attribute__((aligned(16))) _Float16 sa[2][TM * P];
+  __shared__ __attribute__((aligned(16))) _Float16 sb[2][128 * KC];
+  // 16-byte piece p of column c: the pieces move so that neither the writes
+  // (8 columns apart) nor the reads (16 adjacent columns) share banks
+  auto piece = [](int c, int p) { return c * KC + 8 * (p ^ ((c ^ (c >> 3)) & 7)); };
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / WN, wn = wave % WN, li = lane & 15, kg = lane >> 4;
+  const int64_t c0 = (int64_t)blockIdx.x * 128, t0 = (int64_t)blockIdx.z * TM;
+  const int64_t g = c0 / groupsize;
+  const int all = (int)(K / KC);
+  const int kb = (int)((int64_t)all * blockIdx.y / gridDim.y);
+  const int ke = (int)((int64_t)all * (blockIdx.y + 1) / gridDim.y);
+  const int pair = tid >> 4, col = 8 * (tid & 15);  // this thread's rows 2 pair, and columns
+
+  struct Stage {
+    half8 a[AU];
+    uint32_t w[2][W];
+    float s[2], z[2];
+  };
+  auto fetch = [&](Stage& st, int k) {
+    k = min(k, ke - 1);  // (no branch: it would hold up the loads in flight)
+#pragma unroll
+    for (int u = 0; u < AU; ++u)  // rows past the tokens read the last one
+      st.a[u] = *reinterpret_cast<const half8*>(
+          A + min(t0 + 64 * u + (tid >> 3), m - 1) * lda + (int64_t)k * KC + 8 * (tid & 7));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t r = (int64_t)k * KC + 2 * pair + i, rr = min(r, rows - 1);
+#pragma unroll
+      for (int v = 0; v < W; ++v)
+        st.w[i][v] = packed[rr * nw + (c0 + col) * BITS / 32 + v];
+      const float s = scales[rr * ngroups + g], z = zeros[rr * ngroups + g];
+      st.s[i] = r < rows ? s : 0.f;  // (A holds zeros behind the rows)
+      st.z[i] = r < rows ? z : 0.f;
+    }
+  };
+  auto store = [&](const Stage& st, int buf) {
+#pragma unroll
+    for (int u = 0; u < AU; ++u)
+      *reinterpret_cast<half8*>(&sa[buf][(64 * u + (tid >> 3)) * P + 8 * (tid & 7)]) = st.a[u];
+    const h2 base = {(_Float16)-1024.f, (_Float16)-1024.f};
+    auto put = [&](int j, uint32_t bits) {  // column col + j: 1024 + q of both rows
+      const h2 q = __builtin_bit_cast(h2, bits) + base;
+      h2 v;
+      v[0] = (_Float16)(((float)q[0] - st.z[0]) * st.s[0]);
+      v[1] = (_Float16)(((float)q[1] - st.z[1]) * st.s[1]);
+      *reinterpret_cast<h2*>(&sb[buf][piece(col + j, pair >> 2) + 2 * (pair & 3)]) = v;
+    };
+#pragma unroll
+    for (int v = 0; v < W; ++v)
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        // 0x00bb00bb: byte p of the first row's word below, of the second's above
+        const uint32_t b = __builtin_amdgcn_perm(st.w[1][v], st.w[0][v],
+                                                 0x0c000c00u | ((uint32_t)(4 + p) << 16) | p);
+        if constexpr (BITS == 4) {
+          put(2 * p, (b & 0x000F000Fu) | 0x64006400u);
+          put(2 * p + 1, ((b >> 4) & 0x000F000Fu) | 0x64006400u);
+        } else {
+          put(4 * v + p, b | 0x64006400u);
+        }
+      }
+  };
+  f32x4 acc[4][BT];
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < BT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](int buf) {
+#pragma unroll
+    for (int s = 0; s < KC / 32; ++s) {
+      half8 bf[BT];
+#pragma unroll
+      for (int b = 0; b < BT; ++b)
+        bf[b] = *reinterpret_cast<const half8*>(
+            &sb[buf][piece(16 * (BT * wn + b) + li, 4 * s + kg)]);
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const half8 af = *reinterpret_cast<const half8*>(
+            &sa[buf][(64 * wm + 16 * a + li) * P + 32 * s + 8 * kg]);
+#pragma unroll
+        for (int b = 0; b < BT; ++b)
+          acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(af, bf[b], acc[a][b], 0, 0, 0);
+      }
+    }
+  };
+  Stage s0, s1;
+  fetch(s0, kb);
+  fetch(s1, kb + 1);
+  store(s0, 0);  // kb < ke: every split has a stage
+  fetch(s0, kb + 2);
+  __syncthreads();
+  for (int k = kb; k < ke; k += 2) {
+    if (k + 1 < ke) store(s1, 1);
+    fetch(s1, k + 3);
+    multiply(0);
+    __syncthreads();
+    if (k + 1 >= ke) break;
+    if (k + 2 < ke) store(s0, 0);
+    fetch(s0, k + 4);
+    multiply(1);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = t0 + 64 * wm + 16 * a + 4 * kg + i;
+      if (t >= m) continue;
+#pragma unroll
+      for (int b = 0; b < BT; ++b)
+        sums[((int64_t)blockIdx.y * m + t) * n + c0 + 16 * (BT * wn + b) + li] = acc[a][b][i];
+    }
+}
+
 // A block of tiles per XCD that is as near a square as 1, 2, 4 or 8 XCDs along
 // the tokens make it.
 TileGrid gemm_grid(int64_t ntm, int64_t ntn) {
@@ -452,11 +593,33 @@ bool large_tiles(int64_t m, int64_t n) {
   return 5 * large <= 2 * small;
 }
 
+hipError_t launch_words(const _Float16* A, int64_t lda, int64_t m, const StoredWeights& w,
+                        int64_t K, int splits, float* sums, hipStream_t s) {
+  const int wm = m <= 64 ? 1 : 2;
+  const dim3 grid((unsigned)(w.cols / 128), (unsigned)splits, (unsigned)ceil_div(m, 64 * wm));
+#define GPTQ_WORDS(BITS, WM)                                                                     \
+  hipLaunchKernelGGL((gemm_words_kernel<BITS, WM>), grid, dim3(512), 0, s, A, lda, m, w.packed,  \
+                     packed_words(w.cols, w.bits), w.rows, w.cols, K, w.scales, w.zeros,         \
+                     ceil_div(w.cols, w.groupsize), w.groupsize, sums)
+  if (w.bits == 4 && wm == 1) GPTQ_WORDS(4, 1);
+  else if (w.bits == 4) GPTQ_WORDS(4, 2);
+  else if (wm == 1) GPTQ_WORDS(8, 1);
+  else GPTQ_WORDS(8, 2);
+#undef GPTQ_WORDS
+  return hipGetLastError();
+}
+
 template <int MODE>
 hipError_t launch_gemm(const _Float16* A, int64_t lda, int64_t m, const _Float16* B, int64_t ldb,
-                       int64_t n, int64_t K, const GemmOut& o, hipStream_t s) {
-  const int splits = gemm_splits(m, n, K);
-  if (splits > 1) {
+                       int64_t n, int64_t K, const StoredWeights* w, const GemmOut& o,
+                       hipStream_t s) {
+  const int splits = w != nullptr ? words_splits(m, n, K) : gemm_splits(m, n, K);
+  if (w != nullptr) {
+    const hipError_t e = launch_words(A, lda, m, *w, K, splits, o.sums, s);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(gemm_reduce_kernel<MODE>, dim3((unsigned)m, (unsigned)ceil_div(n, 256)),
+                       dim3(256), 0, s, splits, m, n, o);
+  } else if (splits > 1) {
     const TileGrid g = gemm_grid(ceil_div(m, 128), ceil_div(n, 128));
     hipLaunchKernelGGL((gemm_nt_kernel<4, 2, 3, kSplit>),
                        dim3((unsigned)g.blocks(), (unsigned)splits), dim3(512), 0, s, A, lda, m, B,
@@ -478,6 +641,28 @@ hipError_t launch_gemm(const _Float16* A, int64_t lda, int64_t m, const _Float16
 }
 
 }  // namespace
+
+// One tile of tokens (128): straight from the words, 15 to 43 us instead of 28
+// to 70 for the layers 4096 x 4096 to 32000 x 2048 at 4 bits, 15 to 46 instead
+// of 29 to 87 at 8.  Two tiles round the weights twice: 27 instead of 33 us at
+// 160 tokens x 4096 x 4096 and 68 instead of 76 at 32000 x 2048, but 69 instead
+// of 60 at 4096 x 11008, whose 172 workgroups leave a third of the CUs idle
+// (the copy's tiles are finer), so they have to fill three quarters of them.
+bool words_ok(int64_t m, int bits, int64_t cols, int groupsize, const int* g_idx) {
+  if ((bits != 4 && bits != 8) || g_idx != nullptr || cols % 128 != 0 ||
+      (groupsize % 128 != 0 && groupsize < cols))
+    return false;
+  if (m <= 128) return true;
+  const int64_t tiles = 2 * (cols / 128), wgs = tiles < 256 ? 256 / tiles * tiles : tiles;
+  return m <= 256 && 4 * wgs >= 3 * round_up(wgs, 256);
+}
+
+int words_splits(int64_t m, int64_t n, int64_t K) {
+  const int64_t tiles = ceil_div(m, m <= 64 ? 64 : 128) * (n / 128);
+  int64_t s = 256 / (tiles > 0 ? tiles : 1);
+  if (s > K / KC / 4) s = K / KC / 4;
+  return s < 1 ? 1 : (int)s;
+}
 
 int gemm_splits(int64_t m, int64_t n, int64_t K) {
   const int64_t tiles = ceil_div(m, 128) * ceil_div(n, 128);
@@ -526,8 +711,9 @@ hipError_t launch_prepare(const uint32_t* packed, int bits, int64_t rows, int64_
   const bool words = g_idx == nullptr && (bits == 4 || bits == 8) &&
                      (groupsize % (32 / bits) == 0 || groupsize >= cols);
   p.wt_x = kp / 64;
-  p.wt_blocks = p.wt_x * (words ? ceil_div(p.nw, 32) : ceil_div(cols, 64));
+  p.wt_blocks = wt == nullptr ? 0 : p.wt_x * (words ? ceil_div(p.nw, 32) : ceil_div(cols, 64));
   const dim3 grid((unsigned)(p.count + p.bt_blocks + p.at_blocks + p.wt_blocks));
+  if (grid.x == 0) return hipSuccess;
   if (words && bits == 4) hipLaunchKernelGGL(prepare_kernel<4>, grid, dim3(256), 0, s, p);
   else if (words) hipLaunchKernelGGL(prepare_kernel<8>, grid, dim3(256), 0, s, p);
   else hipLaunchKernelGGL(prepare_kernel<0>, grid, dim3(256), 0, s, p);
@@ -542,19 +728,21 @@ hipError_t launch_pad_rows(const _Float16* src, int64_t lds, int64_t m, int64_t 
 }
 
 hipError_t launch_gemm_nt_f16(const _Float16* A, int64_t lda, int64_t m, const _Float16* B,
-                              int64_t ldb, int64_t n, int64_t K, const AdapterTile* ad,
+                              int64_t ldb, int64_t n, int64_t K, const StoredWeights* w,
+                              const AdapterTile* ad,
                               float* sums, _Float16* C, int64_t ldc, hipStream_t s) {
   GemmOut o{};
   o.sums = sums;
   o.c16 = C;
   o.ldc = ldc;
-  if (ad == nullptr) return launch_gemm<kStore>(A, lda, m, B, ldb, n, K, o, s);
+  if (ad == nullptr) return launch_gemm<kStore>(A, lda, m, B, ldb, n, K, w, o, s);
   o.ad = *ad;
-  return launch_gemm<kStoreAdapters>(A, lda, m, B, ldb, n, K, o, s);
+  return launch_gemm<kStoreAdapters>(A, lda, m, B, ldb, n, K, w, o, s);
 }
 
 hipError_t launch_gemm_nt_acc(const _Float16* A, int64_t lda, int64_t m, const _Float16* B,
-                              int64_t ldb, int64_t n, int64_t K, float* C32,
+                              int64_t ldb, int64_t n, int64_t K, const StoredWeights* w,
+                              float* C32,
                               const float* scale, float* sums, _Float16* C16, int64_t ldc,
                               hipStream_t s) {
   GemmOut o{};
@@ -563,8 +751,8 @@ hipError_t launch_gemm_nt_acc(const _Float16* A, int64_t lda, int64_t m, const _
   o.ldc = ldc;
   o.c32 = C32;
   o.scale = scale;
-  if (C16 == nullptr) return launch_gemm<kAccumulate>(A, lda, m, B, ldb, n, K, o, s);
-  return launch_gemm<kFinish>(A, lda, m, B, ldb, n, K, o, s);
+  if (C16 == nullptr) return launch_gemm<kAccumulate>(A, lda, m, B, ldb, n, K, w, o, s);
+  return launch_gemm<kFinish>(A, lda, m, B, ldb, n, K, w, o, s);
 }
 
 }  // namespace gptq

@@ -43,7 +43,9 @@ int rank_pitch(int rank) { return (int)round_up(rank, 16); }
 // the sums of a split product
 int64_t split_sums(int64_t m, int64_t n, int64_t K) {
   const int splits = gemm_splits(m, n, K);
-  return splits > 1 ? splits * m * n : 0;
+  const int64_t copy = splits > 1 ? splits * m * n : 0;
+  const int64_t words = words_ok(m, 4, n, 128, nullptr) ? words_splits(m, n, K) * m * n : 0;
+  return copy > words ? copy : words;
 }
 
 // The pitch of a matrix of the workspace whose rows the fp16 product reads 64
@@ -316,6 +318,8 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
   _Float16* wt = reinterpret_cast<_Float16*>(ws + L.wt);
   const _Float16* g = reinterpret_cast<const _Float16*>(dy);
   int64_t ldg = lddy;
+  const StoredWeights stored{packed, bits, rows, cols, scales, zeros, groupsize};
+  const bool words = words_ok(m, bits, cols, groupsize, g_idx);
   if (L.kp != rows) {
     _Float16* p = reinterpret_cast<_Float16*>(ws + L.dyp);
     GPTQ_TRY(launch_pad_rows(g, lddy, m, rows, L.kp, L.ldt, p, s));
@@ -336,7 +340,7 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
                              reinterpret_cast<const _Float16*>(ad->A), rank_pitch(rank), at,
                              ad->index, m, list, chunks, ranges};
     GPTQ_TRY(launch_prepare(packed, bits, rows, cols, scales, zeros, groupsize, g_idx, L.kp, L.ldt,
-                            wt, &pa, s));
+                            words ? nullptr : wt, &pa, s));
     const ShrinkJob jx = forward_job(ad, x, ldx, cols, v);
     ShrinkJob jy = jx;  // dv = s dy B, over the rows
     jy.x = g;
@@ -369,11 +373,12 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
     tile.up = at;
     tile.stride = cols * rank_pitch(rank);
     tile.ns = rank_pitch(rank);
-  } else {
+  } else if (!words) {
     GPTQ_TRY(launch_prepare(packed, bits, rows, cols, scales, zeros, groupsize, g_idx, L.kp, L.ldt,
                             wt, nullptr, s));
   }
-  GPTQ_TRY(launch_gemm_nt_f16(g, ldg, m, wt, L.ldt, cols, L.kp, ad != nullptr ? &tile : nullptr,
+  GPTQ_TRY(launch_gemm_nt_f16(g, ldg, m, wt, L.ldt, cols, L.kp, words ? &stored : nullptr,
+                              ad != nullptr ? &tile : nullptr,
                               reinterpret_cast<float*>(ws + L.sums),
                               reinterpret_cast<_Float16*>(dx), lddx, s));
   return GPTQ_OK;
@@ -490,9 +495,14 @@ gptq_status head_backward(const void* h, int64_t m, int64_t cols, int64_t ldh,
                                  zeros + v0 * ng, groupsize, tg.inv_t, lse_eff + t0,
                                  reinterpret_cast<float*>(ws + L.scales), P, ld, s));
       GPTQ_TRY(launch_head_scatter(tt, mt, rows, v0, w, dz + t0 * top, P, ld, s));
-      GPTQ_TRY(launch_prepare(packed + v0 * nw, bits, w, cols, scales + v0 * ng, zeros + v0 * ng,
-                              groupsize, nullptr, wp, ld, wt, nullptr, s));
-      GPTQ_TRY(launch_gemm_nt_acc(P, ld, mt, wt, ld, cols, wp, acc, gscale + t0,
+      const StoredWeights stored{packed + v0 * nw, bits, w, cols, scales + v0 * ng, zeros + v0 * ng,
+                                 groupsize};
+      const bool words = words_ok(mt, bits, cols, groupsize, nullptr);
+      if (!words)
+        GPTQ_TRY(launch_prepare(packed + v0 * nw, bits, w, cols, scales + v0 * ng, zeros + v0 * ng,
+                                groupsize, nullptr, wp, ld, wt, nullptr, s));
+      GPTQ_TRY(launch_gemm_nt_acc(P, ld, mt, wt, ld, cols, wp, words ? &stored : nullptr, acc,
+                                  gscale + t0,
                                   reinterpret_cast<float*>(ws + L.sums), last ? out : nullptr, lddh,
                                   s));
     }

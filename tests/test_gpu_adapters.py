@@ -325,6 +325,46 @@ def test_backward_large_tiles(env, m, rows, cols):
     _backward(env, Layer(env, rows, cols, 4, 128, 2), m, 3, 16, "runs", seed=m)
 
 
+@pytest.mark.parametrize("m,rows,cols,bits,g,n,rank,kind", [
+    (1, 1, 128, 4, 128, 0, 0, ""),               # the smallest: one stage, one row of it
+    (1, 129, 256, 8, 128, 0, 0, ""),             # an odd last pair of rows
+    (64, 640, 384, 4, 128, 2, 16, "mixed"),      # whole 64-token tile, splits of the rows
+    (65, 1003, 512, 8, 256, 0, 0, ""),           # one past it; groups over two tiles of columns
+    (128, 512, 640, 8, 0, 3, 7, "mixed"),        # per-channel
+    (129, 512, 16384, 4, 128, 0, 0, ""),         # two tiles of tokens, 256 workgroups, no split
+    (256, 320, 8192, 8, 128, 2, 8, "runs"),      # the most tokens, two splits at most
+    (160, 256, 11008, 4, 128, 0, 0, ""),         # idle CUs: from the transposed copy
+    (257, 256, 128, 4, 128, 0, 0, ""),           # one past the most tokens
+])
+def test_backward_of_few_tokens(env, m, rows, cols, bits, g, n, rank, kind):
+    """Straight from the packed words up to 256 tokens, and its neighbours."""
+    _backward(env, Layer(env, rows, cols, bits, g, m + rows), m, n, rank, kind, seed=m + cols)
+
+
+def test_backward_takes_any_zeros(env):
+    """Zeros that are no integers (a layer from elsewhere): the packed words
+    and the transposed copy make the same weights of them, so a token alone and
+    the same token among 257 differ by the order of fp32 sums alone:
+    2 * rows * 2^-24 * sum |dy W| (each side is within rows half steps of the
+    exact sum) and one rounding to fp16 each."""
+    torch, gq = env
+    L = Layer(env, 256, 512, 4, 128, 9)
+    packed, bits, cols, scales, zeros, groupsize = L.args
+    zeros = zeros + 0.37
+    rng = np.random.default_rng(9)
+    dy = rng.standard_normal((257, 256)).astype(np.float16)
+    few = gq.linear_backward(_cuda(env, dy[:3]), packed, bits, cols, scales, zeros, groupsize)
+    many = gq.linear_backward(_cuda(env, dy), packed, bits, cols, scales, zeros, groupsize)[:3]
+    eye = torch.eye(256, dtype=torch.float16, device="cuda")
+    W = gq.linear_backward(torch.cat([eye, eye[:1]]), packed, bits, cols, scales, zeros,
+                           groupsize)[:256].double().cpu().numpy()
+    mag = np.abs(dy[:3].astype(np.float64)) @ np.abs(W)
+    few, many = few.double().cpu().numpy(), many.double().cpu().numpy()
+    assert np.all(np.abs(few - many) <= 2 * 256 * 2.0**-24 * mag + 2 * 2.0**-11 * np.abs(many) + 2.0**-24)
+    exact = dy[:3].astype(np.float64) @ W  # of the weights rounded to fp16, as both use them
+    assert np.all(np.abs(few - exact) <= 256 * 2.0**-24 * mag + 2.0**-11 * np.abs(exact) * 1.001 + 2.0**-25)
+
+
 def test_gradients_without_tokens_are_zero(env):
     torch, gq = env
     L = Layer(env, 64, 128, 4, 128, 1)
