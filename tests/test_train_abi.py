@@ -125,7 +125,9 @@ def test_head_refusals(kind):
 def test_workspace_sizes():
     wb, hb = gq.adapters_workspace_bytes, gq.head_workspace_bytes
     assert wb(gq.OP_FORWARD_ADAPTERS, 100, 64, 64, 2, 17) == 100 * 32 * 4
-    assert wb(gq.OP_BACKWARD, 100, 64, 128) == 128 * (64 + 128) * 2
+    copy = 128 * (64 + 128) * 2  # the transposed weights, padded rows
+    assert wb(gq.OP_BACKWARD, 300, 64, 128) == copy
+    assert wb(gq.OP_BACKWARD, 100, 64, 128) == copy + 100 * 128 * 4  # few tokens: fp32 sums too
     assert wb(gq.OP_BACKWARD, 0, 64, 128, 2, 8) == 0
     for a in ((gq.OP_BACKWARD, -1, 64, 64, 1, 8), (gq.OP_BACKWARD, 4, 0, 64, 1, 8),
               (gq.OP_BACKWARD, 4, 64, 64, 1, 129), (gq.OP_BACKWARD, 4, 64, 64, 4097, 8),
