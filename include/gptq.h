@@ -480,7 +480,8 @@ gptq_status gptq_dequant_gemm_adapters(const void* x, int64_t m, int64_t cols, i
  * y = act(x W_hat^T + adapters).  The layer's part is within
  * (cols + 2 ngroups + 2) * 2^-24 * sum_c |x_c| |code_c - zero| scale (the sums
  * may be kept in units of the current group's scale, and added in another
- * order than gptq_linear_forward adds them).  The adapter's part is as above,
+ * order than gptq_linear_forward adds them; a scale below 2^-60 may count as
+ * 0).  The adapter's part is as above,
  * with A x held to 2^-23 of the largest of 16 of its values.  Their fp32 sum
  * is rounded to fp16 once.
  *   Asynchronous; bitwise deterministic.
@@ -507,7 +508,9 @@ gptq_status gptq_linear_forward_adapters(const void* x, int64_t m, int64_t cols,
  *              rows % 64 == 0 also lddy % 8 == 0 and dy 16-byte aligned, else
  *              GPTQ_ERR_UNSUPPORTED); m at most 2^23.
  *   packed, bits, scales, zeros, groupsize, g_idx   as gptq_dequant_gemm
- *              (bits 2..8, any group size).
+ *              (bits 2..8, any group size).  rows cols / 4096 + count (rows +
+ *              cols) / 256, rounded up, must stay below 2^24 (else
+ *              GPTQ_ERR_UNSUPPORTED).
  *   adapters   NULL: dx = W_hat^T dy alone; x, dA and dB are not read.
  *   x          m x cols fp16, the forward product's input.
  *   dx         m x cols fp16 out, row t at dx + t*lddx.

@@ -575,16 +575,29 @@ def _adapters(A, B, scaling, index, m, rows, cols, dev):
     return _Adapters(A.data_ptr(), B.data_ptr(), scaling.data_ptr(), index.data_ptr(), count, rank)
 
 
-def _out_rows(out, m, n, dtype, dev):
+def _new(shape, dtype, dev, stream, result=True):
+    """Memory for work on `stream`, from that stream's own pool: the current
+    stream's may hand out blocks that its own queued work still uses. For a
+    result the caller's stream is recorded, since it is read and freed there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if result:
+        t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
+def _out_rows(out, m, n, dtype, dev, stream):
     """(out, its row stride), allocated when None."""
     if out is None:
-        return torch.empty((m, n), dtype=dtype, device=dev), n
+        return _new((m, n), dtype, dev, stream), n
     return out, _rows_of(out, m, n, dtype, dev, "out")
 
 
-def _out_exactly(out, shape, dtype, dev, name):
+def _out_exactly(out, shape, dtype, dev, name, stream):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return _new(shape, dtype, dev, stream)
     _exactly(out, shape, dtype, dev, name)
     return out
 
@@ -594,13 +607,11 @@ def _launch(fn, args, nbytes, dev, workspace, stream):
     ws = None
     if nbytes > 0:
         if workspace is None:
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            # freed on return, for the next work on the same stream
+            ws = _new(nbytes, torch.uint8, dev, stream, False)
             if ws.data_ptr() % 256:  # another allocator than torch's own
-                ws, _ = _workspace(nbytes, ws.device)
-            if stream is not None:
-                # freed on return: the allocator must not hand it on before
-                # the work queued on `stream` is done
-                ws.record_stream(stream)
+                ws = _new(nbytes + 256, torch.uint8, dev, stream, False)
+                ws = ws[-ws.data_ptr() % 256:]
         else:
             ws, nbytes = _workspace(nbytes, torch.device("cuda", dev), workspace, stream)
     if stream is not None:
@@ -628,7 +639,7 @@ def dequant_gemm_adapters(x, packed, bits: int, cols: int, scales, zeros, groups
     m, ldx, dev = _input(x, cols, "x")
     rows, groupsize = _layer(packed, bits, cols, scales, zeros, groupsize, dev, g_idx)
     ad = _adapters(A, B, scaling, index, m, rows, cols, dev)
-    out, ldy = _out_rows(out, m, rows, _f32, dev)
+    out, ldy = _out_rows(out, m, rows, _f32, dev, stream)
     _launch(lib.gptq_dequant_gemm_adapters,
             (x.data_ptr(), m, cols, ldx, packed.data_ptr(), bits, rows, scales.data_ptr(),
              zeros.data_ptr(), groupsize, g_idx.data_ptr() if g_idx is not None else None, ad,
@@ -646,7 +657,7 @@ def linear_forward_adapters(x, packed, bits: int, cols: int, scales, zeros, grou
     m, ldx, dev = _input(x, cols, "x")
     rows, groupsize = _layer(packed, bits, cols, scales, zeros, groupsize, dev)
     ad = _adapters(A, B, scaling, index, m, rows, cols, dev)
-    out, ldy = _out_rows(out, m, rows, _f16, dev)
+    out, ldy = _out_rows(out, m, rows, _f16, dev, stream)
     _launch(lib.gptq_linear_forward_adapters,
             (x.data_ptr(), m, cols, ldx, packed.data_ptr(), bits, rows, scales.data_ptr(),
              zeros.data_ptr(), groupsize, 1 if relu else 0, ad, out.data_ptr(), ldy),
@@ -662,7 +673,7 @@ def linear_backward(dy, packed, bits: int, cols: int, scales, zeros, groupsize: 
     m, lddy, dev = _input(dy, None, "dy")
     rows, groupsize = _layer(packed, bits, cols, scales, zeros, groupsize, dev, g_idx)
     _rows_of(dy, m, rows, _f16, dev, "dy")
-    out, lddx = _out_rows(out, m, cols, _f16, dev)
+    out, lddx = _out_rows(out, m, cols, _f16, dev, stream)
     _launch(lib.gptq_linear_backward,
             (dy.data_ptr(), m, rows, lddy, packed.data_ptr(), bits, cols, scales.data_ptr(),
              zeros.data_ptr(), groupsize, g_idx.data_ptr() if g_idx is not None else None, None,
@@ -683,9 +694,9 @@ def linear_backward_adapters(dy, x, packed, bits: int, cols: int, scales, zeros,
     _rows_of(dy, m, rows, _f16, dev, "dy")
     ldx = _rows_of(x, m, cols, _f16, dev, "x")
     ad = _adapters(A, B, scaling, index, m, rows, cols, dev)
-    out, lddx = _out_rows(out, m, cols, _f16, dev)
-    dA = _out_exactly(dA, tuple(A.shape), _f32, dev, "dA")
-    dB = _out_exactly(dB, tuple(B.shape), _f32, dev, "dB")
+    out, lddx = _out_rows(out, m, cols, _f16, dev, stream)
+    dA = _out_exactly(dA, tuple(A.shape), _f32, dev, "dA", stream)
+    dB = _out_exactly(dB, tuple(B.shape), _f32, dev, "dB", stream)
     _launch(lib.gptq_linear_backward,
             (dy.data_ptr(), m, rows, lddy, packed.data_ptr(), bits, cols, scales.data_ptr(),
              zeros.data_ptr(), groupsize, g_idx.data_ptr() if g_idx is not None else None, ad,
@@ -721,9 +732,9 @@ def _head_forward(fn, h, layer, index, logits, more, loss, lse, zk, workspace, s
     m, ldh, dev = _input(h, cols, "h")
     rows, groupsize = _layer(packed, bits, cols, scales, zeros, groupsize, dev)
     shape = _head_entries(index, logits, m, dev)
-    loss = _out_exactly(loss, (m,), _f32, dev, "loss")
-    lse = _out_exactly(lse, (m,), _f32, dev, "lse")
-    zk = _out_exactly(zk, shape, _f32, dev, "the entries' logits")
+    loss = _out_exactly(loss, (m,), _f32, dev, "loss", stream)
+    lse = _out_exactly(lse, (m,), _f32, dev, "lse", stream)
+    zk = _out_exactly(zk, shape, _f32, dev, "the entries' logits", stream)
     _launch(fn, (h.data_ptr(), m, cols, ldh, packed.data_ptr(), bits, rows, scales.data_ptr(),
                  zeros.data_ptr(), groupsize, index.data_ptr(), *more, loss.data_ptr(),
                  lse.data_ptr(), zk.data_ptr()),
@@ -739,7 +750,7 @@ def _head_backward(fn, h, layer, index, logits, more, lse, zk, dloss, out, works
     _exactly(lse, (m,), _f32, dev, "lse")
     _exactly(zk, shape, _f32, dev, "the entries' logits")
     _exactly(dloss, (m,), _f32, dev, "dloss")
-    out, lddh = _out_rows(out, m, cols, _f16, dev)
+    out, lddh = _out_rows(out, m, cols, _f16, dev, stream)
     _launch(fn, (h.data_ptr(), m, cols, ldh, packed.data_ptr(), bits, rows, scales.data_ptr(),
                  zeros.data_ptr(), groupsize, index.data_ptr(), *more, lse.data_ptr(),
                  zk.data_ptr(), dloss.data_ptr(), out.data_ptr(), lddh),

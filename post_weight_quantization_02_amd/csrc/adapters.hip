@@ -271,8 +271,8 @@ __global__ __launch_bounds__(256) void grad_reduce_kernel(GradJob g0, GradJob g1
 }
 
 __global__ __launch_bounds__(256) void fill_zero_kernel(float* p, int64_t n) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < n) p[i] = 0.f;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    p[i] = 0.f;
 }
 
 bool vec_ok(const void* p, int64_t ld, int64_t K) {
@@ -376,7 +376,8 @@ hipError_t launch_grads(const GradJob& g0, const GradJob& g1, int64_t m, int64_t
 
 hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t s) {
   if (n == 0) return hipSuccess;
-  hipLaunchKernelGGL(fill_zero_kernel, dim3((unsigned)ceil_div(n, 256)), dim3(256), 0, s, p, n);
+  const int64_t blocks = ceil_div(n, 256) < 65536 ? ceil_div(n, 256) : 65536;
+  hipLaunchKernelGGL(fill_zero_kernel, dim3((unsigned)blocks), dim3(256), 0, s, p, n);
   return hipGetLastError();
 }
 

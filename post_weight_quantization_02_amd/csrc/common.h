@@ -203,6 +203,12 @@ struct PrepareAdapters {  // what the adapters' gradients need beside them
   GradChunk* chunks;
   int2* ranges;     // chunks of each adapter: first, number
 };
+// At most the workgroups of launch_prepare; 256 times as many work-items have
+// to stay below 2^32.
+inline int64_t prepare_groups(int64_t rows, int64_t cols, int64_t count) {
+  return ceil_div(rows, 64) * ceil_div(cols, 64) +
+         count * (1 + ceil_div(round_up(rows, 8), 256) + ceil_div(cols, 256));
+}
 // (wt NULL: without the weights)
 hipError_t launch_prepare(const uint32_t* packed, int bits, int64_t rows, int64_t cols,
                           const float* scales, const float* zeros, int groupsize, const int* g_idx,

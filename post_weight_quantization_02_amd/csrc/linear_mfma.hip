@@ -490,15 +490,16 @@ hipError_t launch_tile(const LinearCall& c, const Tail& tail, int splits, hipStr
 
 // The tile by the tokens and outputs: 64 tokens x 128 outputs up to 64 tokens
 // (with four waves of 32 outputs, one per SIMD, building B and multiplying did
-// not overlap: 48 tokens x 32000 x 4096 took 42 us instead of 38); else 128 x 256 (128), or 256 x 256 where that takes
-// less time.  A round of 256 workgroups of the latter takes 1.6 (8 bits: 2.2)
-// times one of the former.
+// not overlap: 48 tokens x 32000 x 4096 took 42 us instead of 38); else 128 x
+// 256 (8 bits: 128), or 256 x 256 where that takes less time.  With 8192
+// columns a round of 256 workgroups of the latter takes 283 us (8 bits: 252),
+// of the former 168 (99): 1.7 (2.5) times as long.
 enum Shape { kFew, kMiddle, kWide };
 Shape shape_of(int bits, int64_t m, int64_t rows) {
   if (m <= 64) return kFew;
   const int64_t middle = ceil_div(m, 128) * ceil_div(rows, bits == 4 ? 256 : 128);
   const int64_t wide = ceil_div(m, 256) * ceil_div(rows, 256);
-  const int cost = bits == 4 ? 16 : 22;
+  const int cost = bits == 4 ? 17 : 25;
   return 10 * ceil_div(middle, 256) >= cost * ceil_div(wide, 256) ? kWide : kMiddle;
 }
 

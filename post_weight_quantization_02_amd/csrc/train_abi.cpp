@@ -16,6 +16,7 @@ constexpr int64_t kMaxDim = 1 << 20;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 constexpr int64_t kMaxTokens = (int64_t)1 << 23;  // token lists hold ints, grids 2^16 chunks
 constexpr int64_t kMaxAdapters = 1 << 20;
+constexpr int64_t kMaxGroups = 1 << 24;    // workgroups of 256 in a launch
 constexpr int64_t kHeadTokens = 8192;      // tokens per pass of the loss's gradient
 
 inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
@@ -298,6 +299,8 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
                         dB == nullptr || !aligned(dA, 4) || !aligned(dB, 4)))
     return GPTQ_ERR_INVALID_ARG;
   if (m > kMaxTokens || (ad != nullptr && (ad->rank > kMaxRank || ad->count > kMaxGradAdapters)))
+    return GPTQ_ERR_UNSUPPORTED;
+  if (prepare_groups(rows, cols, ad != nullptr ? ad->count : 0) >= kMaxGroups)
     return GPTQ_ERR_UNSUPPORTED;
   // dy goes into LDS by 16-byte loads, unless it is copied to padded rows first
   if (m > 0 && rows % kKPad == 0 && (!aligned(dy, 16) || lddy % 8 != 0)) return GPTQ_ERR_UNSUPPORTED;

@@ -437,6 +437,33 @@ def test_same_results_in_any_stream_with_any_workspace_and_again(env):
             assert torch.equal(a, b)
 
 
+def test_memory_for_another_stream_is_not_taken_from_queued_work(env):
+    """A tensor whose copy is still queued on the current stream is freed, and
+    calls on another stream, which does not wait for it, allocate outputs and
+    workspaces of its size: the copy still gets its values."""
+    torch, gq = env
+    L = Layer(env, 192, 256, 4, 128, 1)
+    m = 300
+    rng = np.random.default_rng(3)
+    x = _cuda(env, rng.standard_normal((m, 256)).astype(np.float16))
+    A, B, s = (_cuda(env, a) for a in _adapters(rng, 4, 16, 192, 256))
+    idx = _cuda(env, _index(rng, "mixed", m, 4))
+    want = gq.linear_forward_adapters(x, *L.args, A, B, s, idx)
+    sizes = [gq.adapters_workspace_bytes(gq.OP_FORWARD_ADAPTERS, m, 192, 256, 4, 16), m * 192 * 2]
+    busy = torch.zeros((4096, 4096), device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    olds = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes]
+    for _ in range(20):
+        busy = busy @ busy
+    copies = [o.clone() for o in olds]
+    del olds
+    got = gq.linear_forward_adapters(x, *L.args, A, B, s, idx, stream=side)
+    torch.cuda.synchronize()
+    assert all(bool((c == 7).all()) for c in copies)
+    assert torch.equal(got, want)
+
+
 def test_decode_and_training_step_replayed_from_a_graph(env):
     """Replays with inputs changed in between, other eager work on the same
     library between them, equal the eager results bit for bit."""

@@ -77,6 +77,11 @@ def test_backward_refusals():
     assert _bwd(ad=_ad(count=4097)) == UNSUP
     assert _bwd(dy=FAKE + 2) == UNSUP       # whole 64-row runs are read 16 bytes at a time
     assert _bwd(lddy=65) == UNSUP
+    # more workgroups than a launch takes: the layer's 64 x 64 tiles, or its adapters' rows
+    assert _bwd(rows=2 ** 18, lddy=2 ** 18, cols=2 ** 18, lddx=2 ** 18) == UNSUP
+    big = dict(cols=2 ** 20, ldx=2 ** 20, lddx=2 ** 20)
+    assert _bwd(ad=_ad(count=4096), **big) == UNSUP
+    assert _bwd(ad=_ad(count=2048), **big) == WS
     assert _bwd(rows=63, lddy=65, dy=FAKE + 2) == WS  # other rows are copied: any alignment
     assert _bwd(m=0, dy=None, dx=None) == gq.GPTQ_OK
     need = gq.adapters_workspace_bytes(gq.OP_BACKWARD, 4, 64, 256, 2, 8)
