@@ -86,8 +86,14 @@ __global__ __launch_bounds__(256) void shrink_rows_kernel(ShrinkJob first, Shrin
 
 // v for 16 T tokens per workgroup on v_mfma_f32_16x16x32_f16 (tokens x rank
 // tiles of 16), the eight waves taking every eighth run of 32 of K and their
-// sums added in wave order.  One pass per adapter found among the tokens.
-// Bound by the read of x: U runs are in flight per wave.
+// sums added in wave order.  One pass per adapter found among the tokens, the
+// passes dealt out to gridDim.z workgroups, the second ones first: a tile where
+// one request ends and the next begins has two, and one workgroup for both
+// ends the launch late (8192 tokens, 4096 and 11008 columns: 97 us instead of
+// 64; 417 tokens, 1024 and 7791 columns: 33 instead of 19).  Bound by the reads
+// from the L2, x once and the adapter's rows for every tile (16 tokens of 4096
+// columns at rank 32: 390 KB): U runs are in flight per wave, and twice as many
+// take as long.
 constexpr int kShrinkWaves = 8;
 template <bool VEC, int NB, int U, int T>
 __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_tile_kernel(ShrinkJob j0, ShrinkJob j1,
@@ -106,12 +112,13 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_tile_kernel(ShrinkJo
     x[t] = job.x + min(tok, m - 1) * job.ldx;
   }
   // zeros where a token has no adapter, and behind the rank
-  for (int o = tid; o < 16 * T * job.ldv; o += 64 * W) {
+  for (int o = tid; o < 16 * T * job.ldv && blockIdx.z == 0; o += 64 * W) {
     const int tok = o / job.ldv, j = o % job.ldv;
     if (t0 + tok < m && (j >= job.rank || valid_id(job.index, t0 + tok, job.count) < 0))
       job.v[(t0 + tok) * job.ldv + j] = 0.f;
   }
   int cur = -1;
+  unsigned pass = 0;
   while (true) {
     int next = 0x7fffffff;
 #pragma unroll
@@ -121,6 +128,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_tile_kernel(ShrinkJo
     for (int o = 8; o > 0; o >>= 1) next = min(next, __shfl_xor(next, o, 64));
     cur = __builtin_amdgcn_readfirstlane(next);
     if (cur == 0x7fffffff) break;  // the same in all the waves
+    if (pass++ % gridDim.z != gridDim.z - 1 - blockIdx.z) continue;
     const _Float16* down = job.down + cur * job.stride;
     f32x4 acc[T][NB];
 #pragma unroll
@@ -215,7 +223,7 @@ __global__ __launch_bounds__(256) void grad_chunk_kernel(GradJob g0, GradJob g1,
 #pragma unroll
       for (int i = 1; i < kGradChunk / 64; ++i) mine = q == i ? tok[i] : mine;
       const int64_t t = __shfl(mine, k & 63, 64);
-      r[u] = load8<VEC>(job.right + t * job.ldr, in ? c0 : job.N, job.N);
+      r[u] = load8<VEC>(job.right + t * job.ldr, in ? c0 : job.R, job.R);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
         l[u][b] = in && 16 * (jb + b) < ldv ? job.left[t * ldv + 16 * (jb + b) + li] : 0.f;
@@ -288,14 +296,14 @@ void shrink_tiles(const ShrinkJob& j0, const ShrinkJob* j1, int64_t m, hipStream
   if constexpr (VEC && NB <= 2) {
     if (m >= 32 * 256) {
       hipLaunchKernelGGL((shrink_tile_kernel<VEC, NB, U, 2>),
-                         dim3((unsigned)ceil_div(m, 32), j1 ? 2 : 1), dim3(64 * kShrinkWaves), 0, s,
+                         dim3((unsigned)ceil_div(m, 32), j1 ? 2 : 1, 2), dim3(64 * kShrinkWaves), 0, s,
                          j0, j1 ? *j1 : j0, m);
       return;
     }
   }
   hipLaunchKernelGGL((shrink_tile_kernel<VEC, NB, U, 1>),
-                     dim3((unsigned)ceil_div(m, 16), j1 ? 2 : 1), dim3(64 * kShrinkWaves), 0, s, j0,
-                     j1 ? *j1 : j0, m);
+                     dim3((unsigned)ceil_div(m, 16), j1 ? 2 : 1, 2),
+                     dim3(64 * kShrinkWaves), 0, s, j0, j1 ? *j1 : j0, m);
 }
 
 }  // namespace
@@ -349,7 +357,7 @@ hipError_t launch_grads(const GradJob& g0, const GradJob& g1, int64_t m, int64_t
                         int ldv, const int* list, const GradChunk* chunks, const int2* ranges,
                         hipStream_t s) {
   const int64_t N = g0.N > g1.N ? g0.N : g1.N;
-  const bool vec = vec_ok(g0.right, g0.ldr, g0.N) && vec_ok(g1.right, g1.ldr, g1.N);
+  const bool vec = vec_ok(g0.right, g0.ldr, g0.R) && vec_ok(g1.right, g1.ldr, g1.R);
   const int tiles = ldv / 16, nb = tiles == 1 ? 1 : tiles == 2 ? 2 : 4;
   const int jblocks = (int)ceil_div(tiles, nb);
   const dim3 grid((unsigned)ceil_div(N, 512), (unsigned)grad_chunks(m, count),

@@ -136,6 +136,7 @@ struct GradJob {
   const float* left;
   const _Float16* right;
   int64_t ldr, N;
+  int64_t R;           // N, or more where right goes on in zeros
   float* part;
   float* out;
   int64_t js, cs;

@@ -359,6 +359,7 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
     ga.right = reinterpret_cast<const _Float16*>(x);
     ga.ldr = ldx;
     ga.N = cols;
+    ga.R = cols;
     ga.part = reinterpret_cast<float*>(ws + L.part_a);
     ga.out = dA;
     ga.js = cols;
@@ -367,6 +368,7 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
     gb.right = g;
     gb.ldr = ldg;
     gb.N = rows;
+    gb.R = ldt;
     gb.part = reinterpret_cast<float*>(ws + L.part_b);
     gb.out = dB;
     gb.js = 1;

@@ -305,6 +305,7 @@ def _backward(env, L, m, n, rank, kind, seed, dy_scale=0.05):
     (16, 64, 128, 4, 128, 2, 16, "mixed"),
     (17, 70, 130, 3, 128, 3, 5, "mixed"),        # odd sizes: scalar loads everywhere
     (300, 192, 320, 4, 64, 3, 16, "runs"),       # group 64
+    (530, 203, 264, 4, 128, 6, 24, "mixed"),     # tiles of many adapters; dy copied, wide loads of it
     (513, 256, 256, 8, 128, 2, 40, "runs"),      # three chunks of tokens an adapter
     (600, 64, 640, 5, 256, 2, 128, "mixed"),     # the largest rank
     (257, 1000, 96, 2, 16, 4, 12, "mixed"),
