@@ -738,7 +738,8 @@ def _head_forward(fn, h, layer, index, logits, more, loss, lse, zk, workspace, s
     _launch(fn, (h.data_ptr(), m, cols, ldh, packed.data_ptr(), bits, rows, scales.data_ptr(),
                  zeros.data_ptr(), groupsize, index.data_ptr(), *more, loss.data_ptr(),
                  lse.data_ptr(), zk.data_ptr()),
-            head_workspace_bytes(OP_HEAD_LOSS, m, rows, cols, shape[-1] if more else 1), dev, workspace, stream)
+            head_workspace_bytes(OP_HEAD_LOSS, m, rows, cols, shape[-1] if more else 1), dev,
+            workspace, stream)
     return loss, lse, zk
 
 
@@ -754,7 +755,8 @@ def _head_backward(fn, h, layer, index, logits, more, lse, zk, dloss, out, works
     _launch(fn, (h.data_ptr(), m, cols, ldh, packed.data_ptr(), bits, rows, scales.data_ptr(),
                  zeros.data_ptr(), groupsize, index.data_ptr(), *more, lse.data_ptr(),
                  zk.data_ptr(), dloss.data_ptr(), out.data_ptr(), lddh),
-            head_workspace_bytes(OP_HEAD_BACKWARD, m, rows, cols, shape[-1] if more else 1), dev, workspace, stream)
+            head_workspace_bytes(OP_HEAD_BACKWARD, m, rows, cols, shape[-1] if more else 1), dev,
+            workspace, stream)
     return out
 
 

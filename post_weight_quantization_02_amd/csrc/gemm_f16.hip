@@ -1,6 +1,8 @@
 // The gradient through a stored layer, dx = dy W_hat, and the products of the
 // vocabulary losses' gradient: the stored weights are written once in fp16
-// with the layer's outputs along the fast axis (launch_prepare), and a dense fp16 product C = A B^T over that axis follows.
+// with the layer's outputs along the fast axis (launch_prepare), and a dense
+// fp16 product C = A B^T over that axis follows; few tokens take the weights
+// straight from the packed words instead.
 //
 // W_hat = (code - zero) * scale is formed in fp32 and rounded to fp16 once
 // (at most 2^-11 of its size, 2^-25 below 2^-14); the products are exact in
@@ -14,8 +16,8 @@ namespace {
 
 // ------------------------------------------------------- what goes before
 // One launch writes the transposed weights and, for the adapters' gradients,
-// A and B the other way round and the tokens grouped by adapter: workgroups of one kind
-// after another, the grouping (a few long ones) first.
+// A and B the other way round and the tokens grouped by adapter: workgroups of
+// one kind after another, the grouping (a few long ones) first.
 struct Prepare {
   // the layer
   const uint32_t* packed;

@@ -146,7 +146,8 @@ __device__ inline void issue(const char* xb, const char* wb, const char* szb, in
 template <int BITS>
 __device__ inline void stage_step(int k, int nk, const char* cur, char* nxt, const char* xb,
                                   const char* wb, const char* szb, int64_t szp,
-                                  const Loads<BITS>& l, int gk, Cursor& use, Cursor& iss, int wave, int xo, int wo, int so,
+                                  const Loads<BITS>& l, int gk, Cursor& use, Cursor& iss,
+                                  int wave, int xo, int wo, int so,
                                   f32x4 (&acc)[AT][BT], float (&unit)[BT], half2_t (&mul)[BT],
                                   half2_t (&off)[BT]) {
   using L = Wide<BITS>;

@@ -390,7 +390,9 @@ gptq_status gptq_linear_backward(const void* dy, int64_t m, int64_t rows, int64_
 }
 
 size_t gptq_head_workspace_bytes(int op, int64_t m, int64_t rows, int64_t cols, int top) {
-  if (m < 1 || top < 1 || top > kMaxTop || m > kMaxTokens || rows < 1 || cols < 1 || rows > kMaxDim || cols > kMaxDim) return 0;
+  if (m < 1 || top < 1 || top > kMaxTop || m > kMaxTokens || rows < 1 || cols < 1 ||
+      rows > kMaxDim || cols > kMaxDim)
+    return 0;
   switch (op) {
     case GPTQ_OP_HEAD_LOSS:
       return partials_bytes(m, rows) + align_up((size_t)scales_copy(m, rows, cols) * sizeof(float));
