@@ -195,6 +195,26 @@ def test_forward_with_adapters(env, m, rows, cols, bits, g, n, rank, kind, relu)
     _forward(env, Layer(env, rows, cols, bits, g, m + rows), m, n, rank, kind, relu, seed=m + cols)
 
 
+@pytest.mark.parametrize("cols,bits,g,n,rank,kind,relu", [
+    (128, 4, 0, 2, 8, "runs", True),        # two stages, one group
+    (640, 4, 256, 3, 20, "mixed", False),   # a short last group
+    (384, 8, 128, 2, 16, "runs", False),    # three stages of 150 KB
+    (640, 8, 256, 1, 5, "last", True),
+])
+def test_forward_in_the_largest_tiles(env, cols, bits, g, n, rank, kind, relu):
+    """256 x 256, ragged both ways, with groups that add nothing: their scale
+    is 0, in some rows all of them. The sums keep their unit through those."""
+    L = Layer(env, 4200, cols, bits, g, cols + bits)
+    L.s[::3, -1] = 0
+    L.s[1::3, 0] = 0
+    L.s[5::7] = 0
+    gi = np.arange(cols) // L.gg
+    L.W = (L.codes - L.z[:, gi]) * L.s[:, gi]
+    L.Wmag = (np.abs(L.codes) + np.abs(L.z[:, gi])) * L.s[:, gi]
+    L.args = (*L.args[:3], _cuda(env, L.s, np.float32), *L.args[4:])
+    _forward(env, L, 2100, n, rank, kind, relu, seed=cols)
+
+
 def test_tokens_without_adapter_get_the_layers_own_product(env):
     """Both products may add in another order than without adapters: each is
     within its own bound of the exact sum, the sum of the bounds apart, and
