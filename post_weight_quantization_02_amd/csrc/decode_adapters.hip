@@ -251,6 +251,7 @@ __global__ __launch_bounds__(256) void decode_rows_kernel(
   constexpr int K = 32 / BITS;
   constexpr uint32_t MASK = (1u << BITS) - 1u;
   constexpr int TW = 4096 / K;  // words per pass
+  constexpr int U = 16 / MT;
   __shared__ _Float16 xs[MT][TW * K];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t r = (int64_t)blockIdx.x * 4 + wave;
@@ -261,11 +262,21 @@ __global__ __launch_bounds__(256) void decode_rows_kernel(
   for (int64_t w0 = 0; w0 < nw; w0 += TW) {
     const int words = (int)min((int64_t)TW, nw - w0);
     __syncthreads();
-    for (int t = 0; t < m; ++t)
-      for (int c = tid; c < words * K; c += 256) {
-        const int64_t col = w0 * K + c;
-        xs[t][c] = col < cols ? x[t * ldx + col] : (_Float16)0.f;
-      }
+    for (int c0 = tid; c0 < words * K; c0 += 256 * U) {  // 16 loads in flight
+      _Float16 v[U][MT];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          const int64_t col = w0 * K + c0 + 256 * u;
+          v[u][t] = t < m && col < cols ? x[t * ldx + col] : (_Float16)0.f;
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+          if (t < m && c0 + 256 * u < words * K) xs[t][c0 + 256 * u] = v[u][t];
+    }
     __syncthreads();
     for (int w = lane; w < words; w += 64) {
       const uint32_t q = packed[rr * nw + w0 + w];
